@@ -25,6 +25,7 @@ DORA_F32, DORA_BF16 = 0, 1
 DORA_MAX_RANK = 512
 DORA_MAX_GROUP = 1024
 DORA_MAX_COMPOSE_GROUP = 64
+DORA_MAX_I8_K = 131071
 
 # Symbols include/dora.h declares (the ABI test checks the library exports each).
 EXPORTED = (
@@ -38,7 +39,8 @@ EXPORTED = (
     "dora_compose_fwd_grouped", "dora_compose_bwd_grouped_workspace_size",
     "dora_compose_bwd_grouped", "dora_merge_weight_workspace_size", "dora_merge_weight",
     "dora_factored_norm_sq", "dora_norm_finalize", "dora_compose_fwd_delta",
-    "dora_norm_plan_check",
+    "dora_norm_plan_check", "dora_quantize_rows", "dora_rmsnorm_quant",
+    "dora_linear_i8_workspace_size", "dora_linear_i8",
 )
 
 
@@ -158,6 +160,16 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.dora_factored_norm_sq.restype = c_i
         lib.dora_norm_finalize.argtypes = [c_vp, c_vp, c_f, c_i64, c_vp, c_vp, c_vp]
         lib.dora_norm_finalize.restype = c_i
+        lib.dora_quantize_rows.argtypes = [c_vp, c_i, c_i64, c_i64, c_vp, c_vp, c_vp]
+        lib.dora_quantize_rows.restype = c_i
+        lib.dora_rmsnorm_quant.argtypes = [c_vp, c_vp, c_vp, c_f, c_i, c_i64, c_i64, c_vp, c_vp,
+                                           c_vp, c_vp]
+        lib.dora_rmsnorm_quant.restype = c_i
+        lib.dora_linear_i8_workspace_size.argtypes = [c_i64, c_i64, c_i64]
+        lib.dora_linear_i8_workspace_size.restype = c_sz
+        lib.dora_linear_i8.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_i, c_i64, c_i64, c_i64,
+                                       c_vp, c_vp, c_sz, c_vp]
+        lib.dora_linear_i8.restype = c_i
         _lib = lib
         return lib
 
@@ -585,3 +597,118 @@ def dora_norm_finalize(sq: torch.Tensor, m: Optional[torch.Tensor] = None, eps: 
         _dev(g_out if m is not None else None, "g_out", torch.float32, (d_out,)),
         _stream(stream)), "dora_norm_finalize")
     return n_out, (g_out if m is not None else None)
+
+
+# ------------------------------------------------- 8-bit serving of a merged weight
+
+def _here(t: torch.Tensor, name: str) -> torch.device:
+    """The device of a call's first operand, which must be the current one (the
+    library launches there); the other operands are checked against it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (got {dev})")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev} but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _on(dev: torch.device, t: Optional[torch.Tensor], name: str, dtype, shape) -> int:
+    """_dev for an operand that must be on `dev`."""
+    if t is not None and isinstance(t, torch.Tensor) and t.device != dev:
+        raise ValueError(f"{name} must be on {dev} (got {t.device})")
+    return _dev(t, name, dtype, shape)
+
+
+def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+    """An output or workspace, allocated for the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) \
+            else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions (got shape {tuple(t.shape)})")
+    return t.shape
+
+
+def dora_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                       scale: Optional[torch.Tensor] = None, stream=None):
+    """int8 codes and fp32 scales of the rows of x ([rows, cols], fp32 or bf16):
+    x is approximately q * scale[:, None].  Returns (q, scale)."""
+    lib = load_library()
+    dev = _here(x, "x")
+    dt = _dtype_code(x)
+    rows, cols = _matrix(x, "x")
+    q = _new((rows, cols), torch.int8, dev, stream) if q is None else q
+    scale = _new((rows,), torch.float32, dev, stream) if scale is None else scale
+    _check(lib.dora_quantize_rows(
+        _dev(x, "x"), dt, rows, cols, _on(dev, q, "q", torch.int8, (rows, cols)),
+        _on(dev, scale, "scale", torch.float32, (rows,)), _stream(stream)), "dora_quantize_rows")
+    return q, scale
+
+
+def dora_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float,
+                       residual: Optional[torch.Tensor] = None,
+                       h_out: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                       scale: Optional[torch.Tensor] = None, stream=None):
+    """h = x + residual; int8 codes and fp32 scales per token of the RMS norm of
+    h times weight.  Returns (q, scale, h), h None without a residual.  h_out
+    may be x or residual itself."""
+    lib = load_library()
+    dev = _here(x, "x")
+    dt = _dtype_code(x)
+    T, d = _matrix(x, "x")
+    if residual is None and h_out is not None:
+        raise ValueError("h_out is the sum with a residual: pass residual too")
+    if residual is not None and h_out is None:
+        h_out = _new((T, d), x.dtype, dev, stream)
+    q = _new((T, d), torch.int8, dev, stream) if q is None else q
+    scale = _new((T,), torch.float32, dev, stream) if scale is None else scale
+    _check(lib.dora_rmsnorm_quant(
+        _dev(x, "x"), _on(dev, residual, "residual", x.dtype, (T, d)),
+        _on(dev, weight, "weight", x.dtype, (d,)), float(eps), dt, T, d,
+        _on(dev, h_out, "h_out", x.dtype, (T, d)), _on(dev, q, "q", torch.int8, (T, d)),
+        _on(dev, scale, "scale", torch.float32, (T,)), _stream(stream)), "dora_rmsnorm_quant")
+    return q, scale, h_out
+
+
+def dora_linear_i8_workspace_size(T: int, d_out: int, d_in: int) -> int:
+    return int(load_library().dora_linear_i8_workspace_size(T, d_out, d_in))
+
+
+def dora_linear_i8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor,
+                   w_scale: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   dtype: torch.dtype = torch.bfloat16, y: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[t, j] = (xq[t] . wq[j]) x_scale[t] w_scale[j] (+ bias[j]) in `dtype`
+    (bf16 or fp32; y's own where y is given).  xq [T, d_in], wq [d_out, d_in]
+    int8; scales and bias fp32."""
+    lib = load_library()
+    dev = _here(xq, "xq")
+    T, d_in = _matrix(xq, "xq")
+    d_out = _matrix(wq, "wq")[0]
+    if y is None:
+        if dtype not in _DT:
+            raise TypeError(f"unsupported dtype {dtype}: the library takes float32 or bfloat16")
+        y = _new((T, d_out), dtype, dev, stream)
+    dt = _dtype_code(y)
+    need = lib.dora_linear_i8_workspace_size(T, d_out, d_in)
+    if ws is None and need > 0:
+        ws = _new((need,), torch.uint8, dev, stream)
+    _check(lib.dora_linear_i8(
+        _dev(xq, "xq", torch.int8), _on(dev, x_scale, "x_scale", torch.float32, (T,)),
+        _on(dev, wq, "wq", torch.int8, (d_out, d_in)),
+        _on(dev, w_scale, "w_scale", torch.float32, (d_out,)),
+        _on(dev, bias, "bias", torch.float32, (d_out,)), dt, T, d_out, d_in,
+        _on(dev, y, "y", y.dtype, (T, d_out)),
+        0 if ws is None else _on(dev, ws, "ws", None, None),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "dora_linear_i8")
+    return y

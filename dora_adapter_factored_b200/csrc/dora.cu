@@ -18,9 +18,11 @@
 #include "dora.h"
 #include "common.cuh"
 #include "compose.cuh"
+#include "linear_i8.cuh"
 #include "merge.cuh"
 #include "norm_simt.cuh"
 #include "norm_tc.cuh"
+#include "quant.cuh"
 
 namespace dora {
 namespace {
@@ -1941,6 +1943,196 @@ extern "C" dora_status_t dora_compose_bwd_static(const void* dy, const void* bas
   return dora_compose_bwd(dy, base, lora, m, n, s, eps, dt, T, d_out, d_base, d_lora, dm,
                           scratch, kStaticScratchBytes, stream);
 }
+
+// ---------------------------------------------------------------------------
+// 8-bit serving: row quantisation (plain, or behind the RMS norm) and the
+// linear layer on its codes.
+// ---------------------------------------------------------------------------
+namespace dora {
+namespace {
+// Largest number of rows (tokens, output channels) and of columns of a call;
+// keeps the kernels' int indices in range.
+constexpr int64_t kMaxQuantRows = int64_t(1) << 30;
+constexpr int64_t kMaxQuantCols = int64_t(1) << 30;
+
+// Blocks the row kernels keep per SM before they walk rows.
+constexpr int kRowThreadsPerSm = 1024;
+
+template <typename E, int VEC, int MODE>
+void launch_rows(const RowArgs& P, int sms, cudaStream_t cs) {
+  const long long nvec = P.d / VEC;
+  const long long want = ceil_div_ll(ceil_div_ll(nvec, row_nv(VEC)), 32) * 32;
+  const bool fits = want <= kRowThreads;
+  const int threads = static_cast<int>(std::min<long long>(want, kRowThreads));
+  const int by = fits && threads == 32 ? 8 : 1;  // one-warp rows share a block
+  const long long groups = ceil_div_ll(P.rows, by);
+  const int per_sm = std::max(1, kRowThreadsPerSm / (threads * by));
+  const unsigned grid =
+      static_cast<unsigned>(std::min<long long>(groups, static_cast<long long>(sms) * per_sm));
+  if (fits)
+    launch_stream(row_quant_kernel<E, VEC, MODE>, dim3(grid), dim3(threads, by), 0, cs, P);
+  else
+    launch_stream(row_quant_long_kernel<E, VEC, MODE>, dim3(grid), dim3(threads), 0, cs, P);
+}
+
+template <int MODE>
+void launch_rows_dt(const RowArgs& P, dora_dtype_t dt, int sms, cudaStream_t cs) {
+  const int v = dt == DORA_BF16 ? 8 : 4;
+  const bool vec = P.d % v == 0 && aligned16(P.x) && aligned16(P.residual) &&
+                   aligned16(P.weight) && aligned16(P.h_out) &&
+                   (reinterpret_cast<uintptr_t>(P.q) & (v - 1)) == 0;
+  if (dt == DORA_BF16) {
+    if (vec)
+      launch_rows<__nv_bfloat16, 8, MODE>(P, sms, cs);
+    else
+      launch_rows<__nv_bfloat16, 1, MODE>(P, sms, cs);
+  } else {
+    if (vec)
+      launch_rows<float, 4, MODE>(P, sms, cs);
+    else
+      launch_rows<float, 1, MODE>(P, sms, cs);
+  }
+}
+
+// Element alignment of a pointer that may be NULL.
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// The checks both row calls share, then the launch.
+dora_status_t run_rows(const RowArgs& P, dora_dtype_t dt, int mode, dora_stream_t stream) {
+  const size_t es = dt == DORA_BF16 ? 2 : 4;
+  const size_t n = static_cast<size_t>(P.rows) * P.d, nb = n * es;
+  const size_t sb = static_cast<size_t>(P.rows) * 4, wb = static_cast<size_t>(P.d) * es;
+  const void* ins[2] = {P.x, P.residual};
+  if (!aligned_to(P.x, es) || !aligned_to(P.residual, es) || !aligned_to(P.weight, es) ||
+      !aligned_to(P.h_out, es) || !aligned_to(P.scale, 4))
+    return DORA_ERR_INVALID_ARG;
+  if (overlaps(P.q, n, P.scale, sb) || overlaps(P.q, n, P.h_out, nb) ||
+      overlaps(P.scale, sb, P.h_out, nb) || overlaps(P.q, n, P.weight, wb) ||
+      overlaps(P.scale, sb, P.weight, wb) || overlaps(P.h_out, nb, P.weight, wb))
+    return DORA_ERR_INVALID_ARG;
+  for (const void* in : ins) {
+    if (overlaps(P.q, n, in, nb) || overlaps(P.scale, sb, in, nb)) return DORA_ERR_INVALID_ARG;
+    if (P.h_out != in && overlaps(P.h_out, nb, in, nb)) return DORA_ERR_INVALID_ARG;
+  }
+  const DeviceInfo* di = device_info();
+  if (di == nullptr) return DORA_ERR_CUDA;
+  if (!di->supported) return DORA_ERR_UNSUPPORTED;
+  if (P.rows == 0) return DORA_OK;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  TimedLaunch tl(cs);
+  if (mode == kRowQuant)
+    launch_rows_dt<kRowQuant>(P, dt, di->sms, cs);
+  else if (mode == kRowNorm)
+    launch_rows_dt<kRowNorm>(P, dt, di->sms, cs);
+  else
+    launch_rows_dt<kRowNormAdd>(P, dt, di->sms, cs);
+  return launch_status();
+}
+
+// ---- linear layer
+
+template <typename O, int TT>
+void launch_dot(const LinearArgs& P, bool vec, int sms, cudaStream_t cs) {
+  // Warps that share a row's k: as few as give every SM about 16 warps.
+  const long long rows4 = ceil_div_ll(P.d_out, kDotRows);
+  const long long tiles = ceil_div_ll(P.T, TT);
+  int splits = 1;
+  while (splits < kDotWarps && rows4 * tiles * splits < 16ll * sms) splits *= 2;
+  const unsigned gx = static_cast<unsigned>(ceil_div_ll(rows4, kDotWarps / splits));
+  const unsigned gy = static_cast<unsigned>(std::min<long long>(tiles, 65535));
+  if (vec)
+    launch_stream(dot_i8_kernel<O, TT, true>, dim3(gx, gy), dim3(kDotWarps * 32), 0, cs, P, splits);
+  else
+    launch_stream(dot_i8_kernel<O, TT, false>, dim3(gx, gy), dim3(kDotWarps * 32), 0, cs, P,
+                  splits);
+}
+
+template <typename O>
+void launch_linear(const LinearArgs& P, int sms, cudaStream_t cs) {
+  const bool vec = P.d_in % 16 == 0 && aligned16(P.xq) && aligned16(P.wq);
+  if (P.T == 1)
+    launch_dot<O, 1>(P, vec, sms, cs);
+  else if (P.T == 2)
+    launch_dot<O, 2>(P, vec, sms, cs);
+  else if (P.T <= 4)
+    launch_dot<O, 4>(P, vec, sms, cs);
+  else
+    launch_dot<O, kDotTokens>(P, vec, sms, cs);
+}
+}  // namespace
+}  // namespace dora
+
+extern "C" {
+
+dora_status_t dora_quantize_rows(const void* x, dora_dtype_t dt, int64_t rows, int64_t cols,
+                                 int8_t* q, float* scale, dora_stream_t stream) {
+  if (dt != DORA_F32 && dt != DORA_BF16) return DORA_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 1) return DORA_ERR_INVALID_ARG;
+  if (rows > 0 && (x == nullptr || q == nullptr || scale == nullptr)) return DORA_ERR_INVALID_ARG;
+  if (rows > kMaxQuantRows || cols > kMaxQuantCols) return DORA_ERR_UNSUPPORTED;
+  const RowArgs P{x, nullptr, nullptr, nullptr, q, scale, rows, static_cast<int>(cols), 0.f};
+  return run_rows(P, dt, kRowQuant, stream);
+}
+
+dora_status_t dora_rmsnorm_quant(const void* x, const void* residual, const void* weight,
+                                 float eps, dora_dtype_t dt, int64_t T, int64_t d, void* h_out,
+                                 int8_t* q, float* scale, dora_stream_t stream) {
+  if (dt != DORA_F32 && dt != DORA_BF16) return DORA_ERR_INVALID_ARG;
+  if (T < 0 || d < 1 || weight == nullptr) return DORA_ERR_INVALID_ARG;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return DORA_ERR_INVALID_ARG;
+  if (T > 0 && (x == nullptr || q == nullptr || scale == nullptr)) return DORA_ERR_INVALID_ARG;
+  if (T > 0 && (residual == nullptr) != (h_out == nullptr)) return DORA_ERR_INVALID_ARG;
+  if (T > kMaxQuantRows || d > kMaxQuantCols) return DORA_ERR_UNSUPPORTED;
+  const RowArgs P{x, residual, weight, h_out, q, scale, T, static_cast<int>(d), eps};
+  return run_rows(P, dt, residual == nullptr ? kRowNorm : kRowNormAdd, stream);
+}
+
+size_t dora_linear_i8_workspace_size(int64_t T, int64_t d_out, int64_t d_in) {
+  (void)T;
+  (void)d_out;
+  (void)d_in;
+  return 0;
+}
+
+dora_status_t dora_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq,
+                             const float* w_scale, const float* bias, dora_dtype_t dt_out,
+                             int64_t T, int64_t d_out, int64_t d_in, void* y, void* ws,
+                             size_t ws_bytes, dora_stream_t stream) {
+  if (dt_out != DORA_F32 && dt_out != DORA_BF16) return DORA_ERR_INVALID_ARG;
+  if (T < 0 || d_out < 1 || d_in < 1 || wq == nullptr || w_scale == nullptr)
+    return DORA_ERR_INVALID_ARG;
+  if (T > 0 && (xq == nullptr || x_scale == nullptr || y == nullptr)) return DORA_ERR_INVALID_ARG;
+  if (T > kMaxQuantRows || d_out > kMaxQuantRows || d_in > DORA_MAX_I8_K)
+    return DORA_ERR_UNSUPPORTED;
+  const size_t es = dt_out == DORA_BF16 ? 2 : 4;
+  if (!aligned_to(x_scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(bias, 4) ||
+      !aligned_to(y, es))
+    return DORA_ERR_INVALID_ARG;
+  const size_t yb = static_cast<size_t>(T) * d_out * es;
+  if (overlaps(y, yb, xq, static_cast<size_t>(T) * d_in) ||
+      overlaps(y, yb, wq, static_cast<size_t>(d_out) * d_in) ||
+      overlaps(y, yb, x_scale, static_cast<size_t>(T) * 4) ||
+      overlaps(y, yb, w_scale, static_cast<size_t>(d_out) * 4) ||
+      overlaps(y, yb, bias, static_cast<size_t>(d_out) * 4))
+    return DORA_ERR_INVALID_ARG;
+  (void)ws;
+  (void)ws_bytes;
+  const DeviceInfo* di = device_info();
+  if (di == nullptr) return DORA_ERR_CUDA;
+  if (!di->supported) return DORA_ERR_UNSUPPORTED;
+  if (T == 0) return DORA_OK;
+  LinearArgs P{xq, x_scale, wq, w_scale, bias, y, static_cast<int>(T), static_cast<int>(d_out),
+               static_cast<int>(d_in)};
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  TimedLaunch tl(cs);
+  if (dt_out == DORA_BF16)
+    launch_linear<__nv_bfloat16>(P, di->sms, cs);
+  else
+    launch_linear<float>(P, di->sms, cs);
+  return launch_status();
+}
+
+}  // extern "C"
 
 extern "C" {
 

@@ -314,6 +314,68 @@ dora_status_t dora_merge_weight(const void *W0, const void *A, const void *B, co
                                 size_t ws_bytes, dora_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * 8-bit serving of a merged weight.  dora_merge_weight folds the adapter into
+ * one dense weight; these calls hold that weight and its inputs as signed
+ * 8-bit codes with one fp32 scale per row, and multiply the codes:
+ *
+ *   once:      dora_quantize_rows   W' [d_out, d_in]  -> wq, w_scale
+ *   per layer: dora_rmsnorm_quant   hidden states     -> xq, x_scale (and h)
+ *              (or dora_quantize_rows where no norm precedes the layer)
+ *              dora_linear_i8       xq, wq            -> y = x W'^T
+ *
+ * A row v of values is held as  scale = max_j |v_j| / 127  and
+ * q_j = round(v_j / scale), half to even, in [-127, 127]; v_j is then
+ * approximately q_j scale, to half a step.  The quotient is formed as
+ * v_j (127 / max|v|) in fp32, so a value within about 2^-23 of its size from
+ * the middle between two codes may take either.
+ *   - A row whose step max|v| / 127 is below the smallest normal fp32
+ *     (2^-126), an all-zero row among them: codes 0, scale 0.
+ *   - A row with an infinity or a NaN: codes 0, scale NaN, so that the outputs
+ *     computed from it are NaN.  Other rows are not touched by it.
+ * Forward only: no gradient is defined through the codes.
+ * ---------------------------------------------------------------------- */
+
+/* Rows of x [rows, cols] (dtype `dt`) to codes q [rows, cols] and scale
+ * [rows] fp32.  Outputs must not overlap x or each other.  rows == 0 launches
+ * nothing.  rows, cols <= 2^30.  One launch, one pass over x for rows up to
+ * 16384 bf16 or 8192 fp32 elements (half that where rows are not 16-byte
+ * aligned), else two. */
+dora_status_t dora_quantize_rows(const void *x, dora_dtype_t dt, int64_t rows, int64_t cols,
+                                 int8_t *q, float *scale, dora_stream_t stream);
+
+/* RMS norm with the residual's addition and quantised output, per token t:
+ *   h = x + residual, rounded to `dt` and written to h_out (or h = x where
+ *       residual and h_out are both NULL; one without the other is rejected)
+ *   v = h weight / sqrt(mean(h^2) + eps);  q, scale from v as above
+ * The norm is of the stored h.  x, residual, h_out [T, d] and weight [d] in
+ * `dt`; q [T, d]; scale [T] fp32; eps > 0 and finite.  Sums and products are
+ * fp32: a row whose sum of squares, or whose h weight, passes fp32's range
+ * counts as not finite.  h_out may equal x or residual (element for element);
+ * no other overlap.  T == 0 launches nothing.  T, d <= 2^30.  One launch. */
+dora_status_t dora_rmsnorm_quant(const void *x, const void *residual, const void *weight,
+                                 float eps, dora_dtype_t dt, int64_t T, int64_t d, void *h_out,
+                                 int8_t *q, float *scale, dora_stream_t stream);
+
+/* Linear layer on codes:
+ *   y[t, j] = (sum_k xq[t, k] wq[j, k]) x_scale[t] w_scale[j] (+ bias[j])
+ * The sum is exact in int32; it is converted to fp32, multiplied by x_scale,
+ * then by w_scale (with the bias added in the same rounding), and rounded to
+ * dt_out.  Every kernel does the same operations on the same exact sum, so
+ * y is bitwise reproducible and a token's row does not depend on the batch.
+ * xq [T, d_in], wq [d_out, d_in] (any codes, -128 included); x_scale [T],
+ * w_scale, bias [d_out] fp32, bias may be NULL; y [T, d_out] in dt_out
+ * (DORA_F32 or DORA_BF16).  d_in <= DORA_MAX_I8_K; T, d_out <= 2^30
+ * (DORA_ERR_UNSUPPORTED otherwise).  y must not overlap an input.  T == 0
+ * launches nothing.  Workspace: dora_linear_i8_workspace_size() bytes, 256-byte
+ * aligned, contents undefined on entry and exit (0 bytes: ws may be NULL). */
+#define DORA_MAX_I8_K 131071
+size_t dora_linear_i8_workspace_size(int64_t T, int64_t d_out, int64_t d_in);
+dora_status_t dora_linear_i8(const int8_t *xq, const float *x_scale, const int8_t *wq,
+                             const float *w_scale, const float *bias, dora_dtype_t dt_out,
+                             int64_t T, int64_t d_out, int64_t d_in, void *y, void *ws,
+                             size_t ws_bytes, dora_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Compose backward without a workspace (no counterpart on the pages: it is
  * an interface convenience, not part of the method).
  *

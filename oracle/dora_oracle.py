@@ -66,6 +66,9 @@ __all__ = [
     "merged_weight",
     "merge_weight_given_norm",
     "rows_dense_row_norm",
+    "quantize_rows",
+    "rmsnorm",
+    "linear_i8",
 ]
 
 
@@ -277,3 +280,37 @@ def merge_weight_given_norm(W0, A, B, m, n, s: float, eps: float) -> np.ndarray:
     W0, A, B = _f64(W0), _f64(A), _f64(B)
     g, _, _ = magnitude_scale(m, n, eps)
     return g[:, None] * (W0 + s * (B @ A))
+
+
+# --------------------------------------------------------------------------
+# 8-bit serving of a merged weight
+# --------------------------------------------------------------------------
+
+def quantize_rows(v):
+    """Codes, scales and unrounded codes of the rows of v: scale = max|v| / 127,
+    q = rint(v / scale) (half to even).  A row whose step is not a normal
+    fp32 number has scale 0 and codes 0; one that is not finite scale NaN and
+    codes 0."""
+    v = _f64(v)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        scale = np.max(np.abs(v), axis=1) / 127.0
+        finite = np.isfinite(v).all(axis=1)
+        live = finite & (scale >= 2.0 ** -126)
+        u = np.where(live[:, None], v / np.where(live, scale, 1.0)[:, None], 0.0)
+    scale = np.where(finite, np.where(live, scale, 0.0), np.nan)
+    return np.rint(u), scale, u
+
+
+def rmsnorm(h, weight, eps: float):
+    """h weight / sqrt(mean(h^2) + eps) per row."""
+    h = _f64(h)
+    rms = np.sqrt(np.mean(h * h, axis=1, keepdims=True) + eps)
+    return h / rms * _f64(weight)
+
+
+def linear_i8(xq, x_scale, wq, w_scale, bias=None):
+    """The exact integer sums and y = (xq wq^T) x_scale w_scale (+ bias).  Sums of
+    at most 131071 products of 8-bit codes are exact in fp64."""
+    acc = _f64(xq) @ _f64(wq).T
+    y = acc * _f64(x_scale)[:, None] * _f64(w_scale)[None, :]
+    return acc, (y if bias is None else y + _f64(bias)[None, :])
