@@ -314,6 +314,22 @@ bool make_tmap_bf16(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t c
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Row-major matrix of 8-bit codes [rows, cols] with `ld` codes per row, in
+// boxes of box_cols x box_rows with 128-byte swizzle; out-of-range codes read
+// as zero.
+bool make_tmap_i8(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld,
+                  uint32_t box_cols, uint32_t box_rows) {
+  auto enc = tmap_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ------------------------------------------------------------ norm planning
 
 struct ModulePlan {
@@ -711,7 +727,12 @@ bool ensure_tc_attrs() {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem)) !=
           cudaSuccess ||
       (e = cudaFuncSetAttribute(merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kMaxDynSmem)) != cudaSuccess) {
+                                kMaxDynSmem)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(tile_i8_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kTileI8MaxDynSmem)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(tile_i8_kernel<__nv_bfloat16>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kTileI8MaxDynSmem)) != cudaSuccess) {
     note_error("cudaFuncSetAttribute", e);
     return false;
   }
@@ -1954,6 +1975,7 @@ namespace {
 // keeps the kernels' int indices in range.
 constexpr int64_t kMaxQuantRows = int64_t(1) << 30;
 constexpr int64_t kMaxQuantCols = int64_t(1) << 30;
+constexpr int64_t kMaxLinearTokens = int64_t(1) << 23;  // token tiles are a grid's second axis
 
 // Blocks the row kernels keep per SM before they walk rows.
 constexpr int kRowThreadsPerSm = 1024;
@@ -2048,8 +2070,7 @@ void launch_dot(const LinearArgs& P, bool vec, int sms, cudaStream_t cs) {
 }
 
 template <typename O>
-void launch_linear(const LinearArgs& P, int sms, cudaStream_t cs) {
-  const bool vec = P.d_in % 16 == 0 && aligned16(P.xq) && aligned16(P.wq);
+void launch_dot_any(const LinearArgs& P, bool vec, int sms, cudaStream_t cs) {
   if (P.T == 1)
     launch_dot<O, 1>(P, vec, sms, cs);
   else if (P.T == 2)
@@ -2058,6 +2079,129 @@ void launch_linear(const LinearArgs& P, int sms, cudaStream_t cs) {
     launch_dot<O, 4>(P, vec, sms, cs);
   else
     launch_dot<O, kDotTokens>(P, vec, sms, cs);
+}
+
+// The dot-product kernel up to this many tokens, the tensor cores above.
+constexpr int kDotMaxT = 8;
+
+int padded_k(int64_t d_in) { return static_cast<int>(align_up(static_cast<size_t>(d_in), 16)); }
+
+// Bytes of the padded copies of xq and wq, which TMA needs where a row is not
+// a multiple of 16 bytes.
+size_t linear_pad_x(int64_t T, int64_t d_in) {
+  return align_up(static_cast<size_t>(T) * padded_k(d_in), 256);
+}
+bool linear_pads(int64_t T, int64_t d_in) { return T > kDotMaxT && d_in % 16 != 0; }
+
+// Launch with the cluster size of the call and programmatic serialization.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                           unsigned cluster, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    note_error("cluster launch", e);
+    launch_failed = true;
+  }
+  return e;
+}
+
+// Shared memory of a CTA that holds `cols` TMEM columns: at least its share
+// of the SM's 228 KiB, so that CTAs resident together never want more than
+// the 512 columns there are (a CTA waiting for TMEM in one cluster while
+// another waits for that cluster's TMEM would never end), and at least
+// 64 KiB, which does not fit beside a norm or merge CTA.
+constexpr size_t kSmemPerTmemCol = 456;  // 233472 bytes / 512 columns
+size_t tmem_smem_floor(uint32_t cols) {
+  return std::max<size_t>(cols * kSmemPerTmemCol - 1024, size_t(64) << 10);
+}
+
+struct TileI8Plan {
+  int n, tiles_m, tiles_n, splits, stages, kb;
+  uint32_t cols;
+  size_t smem;
+};
+
+TileI8Plan plan_tile_i8(int T, int d_out, int d_in, int sms) {
+  TileI8Plan p;
+  p.tiles_n = static_cast<int>(ceil_div_ll(T, kTileI8MaxN));
+  p.n = round_up_int(static_cast<int>(ceil_div_ll(T, p.tiles_n)), 16);
+  p.tiles_m = static_cast<int>(ceil_div_ll(d_out, kTileI8M));
+  p.kb = static_cast<int>(ceil_div_ll(d_in, kTileI8K));
+  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+  p.splits = 1;
+  while (p.splits < 8 && tiles * p.splits * 2 <= sms && p.kb >= p.splits * 2 * 4) p.splits *= 2;
+  p.cols = 32;
+  while (p.cols < static_cast<uint32_t>(p.n)) p.cols *= 2;
+  // Two CTAs per SM where there are more CTAs than SMs, else one.
+  const size_t stat = 232448 - kTileI8MaxDynSmem;  // the static part
+  const size_t tail = stat + 1024;                 // and the ring's alignment
+  const size_t budget = (tiles * p.splits > sms ? size_t(113) << 10 : size_t(kMaxDynSmem)) - tail;
+  const size_t stage = kTileI8WBytes + static_cast<size_t>(p.n) * kTileI8K;
+  const int kb_cta = static_cast<int>(ceil_div_ll(p.kb, p.splits));
+  p.stages = static_cast<int>(
+      std::min<size_t>({budget / stage, size_t(kTileI8MaxStages), static_cast<size_t>(kb_cta)}));
+  size_t ring = p.stages * stage;
+  if (p.splits > 1) ring = std::max(ring, static_cast<size_t>(p.n) * kTileI8M * 4);
+  p.smem = std::max(ring + 1024, tmem_smem_floor(p.cols) - sizeof(TileI8Tail));
+  return p;
+}
+
+template <typename O>
+dora_status_t launch_tile_i8(const LinearArgs& A, const int8_t* xq, const int8_t* wq, int ld,
+                             int sms, cudaStream_t cs) {
+  const TileI8Plan p = plan_tile_i8(A.T, A.d_out, A.d_in, sms);
+  static thread_local TileI8Dev P;
+  if (!make_tmap_i8(&P.tm_w, wq, A.d_out, ld, ld, kTileI8K, kTileI8M) ||
+      !make_tmap_i8(&P.tm_x, xq, A.T, ld, ld, kTileI8K, p.n))
+    return DORA_ERR_INVALID_ARG;
+  P.a = A;
+  P.n = p.n;
+  P.kb = p.kb;
+  P.splits = p.splits;
+  P.stages = p.stages;
+  P.tmem_cols = p.cols;
+  P.idesc = idesc_i8_s32(kTileI8M, p.n);
+  launch_cluster(tile_i8_kernel<O>, dim3(p.tiles_m * p.splits, p.tiles_n), dim3(kTileI8Threads),
+                 p.smem, p.splits, cs, P, g_timeout_ns.load());
+  return launch_status();
+}
+
+template <typename O>
+dora_status_t launch_linear(const LinearArgs& A, void* ws, int sms, cudaStream_t cs) {
+  const bool vec = A.d_in % 16 == 0 && aligned16(A.xq) && aligned16(A.wq);
+  const bool pads = linear_pads(A.T, A.d_in);
+  // Few tokens; or rows of whole 16-byte steps that start off a boundary,
+  // which TMA cannot read and the workspace (sized from the shape) does not
+  // cover.
+  if (A.T <= kDotMaxT || (!vec && !pads)) {
+    launch_dot_any<O>(A, vec, sms, cs);
+    return launch_status();
+  }
+  if (!pads) return launch_tile_i8<O>(A, A.xq, A.wq, A.d_in, sms, cs);
+  const int ld = padded_k(A.d_in);
+  int8_t* xp = static_cast<int8_t*>(ws);
+  int8_t* wp = xp + linear_pad_x(A.T, A.d_in);
+  const PadArgs px{A.xq, xp, A.T, A.d_in, ld}, pw{A.wq, wp, A.d_out, A.d_in, ld};
+  const long long chunks = static_cast<long long>(std::max(A.T, A.d_out)) * (ld / 16);
+  const unsigned gx = static_cast<unsigned>(
+      std::min<long long>(ceil_div_ll(chunks, kPadThreads), 8ll * sms));
+  launch_stream(pad_rows_kernel, dim3(gx, 2), dim3(kPadThreads), 0, cs, px, pw);
+  const dora_status_t st = launch_status();
+  return st != DORA_OK ? st : launch_tile_i8<O>(A, xp, wp, ld, sms, cs);
 }
 }  // namespace
 }  // namespace dora
@@ -2088,10 +2232,10 @@ dora_status_t dora_rmsnorm_quant(const void* x, const void* residual, const void
 }
 
 size_t dora_linear_i8_workspace_size(int64_t T, int64_t d_out, int64_t d_in) {
-  (void)T;
-  (void)d_out;
-  (void)d_in;
-  return 0;
+  if (T < 1 || d_out < 1 || d_in < 1 || T > kMaxLinearTokens || d_out > kMaxQuantRows ||
+      d_in > DORA_MAX_I8_K || !linear_pads(T, d_in))
+    return 0;
+  return linear_pad_x(T, d_in) + linear_pad_x(d_out, d_in);
 }
 
 dora_status_t dora_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq,
@@ -2102,7 +2246,7 @@ dora_status_t dora_linear_i8(const int8_t* xq, const float* x_scale, const int8_
   if (T < 0 || d_out < 1 || d_in < 1 || wq == nullptr || w_scale == nullptr)
     return DORA_ERR_INVALID_ARG;
   if (T > 0 && (xq == nullptr || x_scale == nullptr || y == nullptr)) return DORA_ERR_INVALID_ARG;
-  if (T > kMaxQuantRows || d_out > kMaxQuantRows || d_in > DORA_MAX_I8_K)
+  if (T > kMaxLinearTokens || d_out > kMaxQuantRows || d_in > DORA_MAX_I8_K)
     return DORA_ERR_UNSUPPORTED;
   const size_t es = dt_out == DORA_BF16 ? 2 : 4;
   if (!aligned_to(x_scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(bias, 4) ||
@@ -2115,21 +2259,26 @@ dora_status_t dora_linear_i8(const int8_t* xq, const float* x_scale, const int8_
       overlaps(y, yb, w_scale, static_cast<size_t>(d_out) * 4) ||
       overlaps(y, yb, bias, static_cast<size_t>(d_out) * 4))
     return DORA_ERR_INVALID_ARG;
-  (void)ws;
-  (void)ws_bytes;
+  const size_t need = dora_linear_i8_workspace_size(T, d_out, d_in);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned256(ws)))
+    return DORA_ERR_WORKSPACE;
+  if (need > 0 && (overlaps(ws, need, y, yb) || overlaps(ws, need, xq, static_cast<size_t>(T) * d_in) ||
+                   overlaps(ws, need, wq, static_cast<size_t>(d_out) * d_in) ||
+                   overlaps(ws, need, x_scale, static_cast<size_t>(T) * 4) ||
+                   overlaps(ws, need, w_scale, static_cast<size_t>(d_out) * 4) ||
+                   overlaps(ws, need, bias, static_cast<size_t>(d_out) * 4)))
+    return DORA_ERR_INVALID_ARG;
   const DeviceInfo* di = device_info();
   if (di == nullptr) return DORA_ERR_CUDA;
   if (!di->supported) return DORA_ERR_UNSUPPORTED;
   if (T == 0) return DORA_OK;
-  LinearArgs P{xq, x_scale, wq, w_scale, bias, y, static_cast<int>(T), static_cast<int>(d_out),
+  if (!ensure_tc_attrs()) return DORA_ERR_CUDA;
+  const LinearArgs P{xq, x_scale, wq, w_scale, bias, y, static_cast<int>(T), static_cast<int>(d_out),
                static_cast<int>(d_in)};
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   TimedLaunch tl(cs);
-  if (dt_out == DORA_BF16)
-    launch_linear<__nv_bfloat16>(P, di->sms, cs);
-  else
-    launch_linear<float>(P, di->sms, cs);
-  return launch_status();
+  return dt_out == DORA_BF16 ? launch_linear<__nv_bfloat16>(P, ws, di->sms, cs)
+                             : launch_linear<float>(P, ws, di->sms, cs);
 }
 
 }  // extern "C"

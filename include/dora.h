@@ -364,7 +364,7 @@ dora_status_t dora_rmsnorm_quant(const void *x, const void *residual, const void
  * y is bitwise reproducible and a token's row does not depend on the batch.
  * xq [T, d_in], wq [d_out, d_in] (any codes, -128 included); x_scale [T],
  * w_scale, bias [d_out] fp32, bias may be NULL; y [T, d_out] in dt_out
- * (DORA_F32 or DORA_BF16).  d_in <= DORA_MAX_I8_K; T, d_out <= 2^30
+ * (DORA_F32 or DORA_BF16).  d_in <= DORA_MAX_I8_K, T <= 2^23, d_out <= 2^30
  * (DORA_ERR_UNSUPPORTED otherwise).  y must not overlap an input.  T == 0
  * launches nothing.  Workspace: dora_linear_i8_workspace_size() bytes, 256-byte
  * aligned, contents undefined on entry and exit (0 bytes: ws may be NULL). */

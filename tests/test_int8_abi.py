@@ -82,7 +82,7 @@ BAD_LINEAR = [
     (dict(sw=None), INVALID), (dict(y=None), INVALID), (dict(dt=3), INVALID),
     (dict(T=-1), INVALID), (dict(d_out=0), INVALID), (dict(d_in=0), INVALID),
     (dict(d_in=131072), UNSUPPORTED),               # the int32 sum could overflow
-    (dict(T=(1 << 30) + 1), UNSUPPORTED), (dict(d_out=(1 << 30) + 1), UNSUPPORTED),
+    (dict(T=(1 << 23) + 1), UNSUPPORTED), (dict(d_out=(1 << 30) + 1), UNSUPPORTED),
     (dict(y=X), INVALID), (dict(y=W), INVALID), (dict(y=R), INVALID), (dict(y=S), INVALID),
     (dict(bias=H), INVALID), (dict(bias=vp(0x7000001)), INVALID), (dict(sx=vp(0x2000002)), INVALID),
     (dict(y=vp(0x4000001)), INVALID), (dict(y=vp(0x4000002), dt=F32), INVALID),
@@ -97,6 +97,24 @@ def test_host_validation(built_library, call, bad):
     for kw, want in bad:
         assert call(lib, **kw) == want, kw
     assert dora.dora_launch_count() == before
+
+
+def test_linear_workspace(built_library):
+    """Copies with rows of 16-byte steps, where the tensor-core path needs them."""
+    lib = dora.load_library(built_library)
+    size = dora.dora_linear_i8_workspace_size
+    assert size(1, 1000, 1003) == 0 and size(300, 1000, 1008) == 0
+    need = size(300, 1000, 1003)
+    assert need == 300 * 1008 + (-300 * 1008) % 256 + 1000 * 1008 + (-1000 * 1008) % 256
+    for bad in ((0, 8, 8), (8, 0, 8), (8, 8, 0), (9, 8, 131072)):
+        assert size(*bad) == 0
+    kw = dict(T=300, d_out=1000, d_in=1003)
+    ws = vp(0x9000000)
+    for bad in (dict(ws=None), dict(nws=need - 1), dict(ws=vp(0x9000010))):
+        assert _linear(lib, **kw, **bad) == _abi.DORA_ERR_WORKSPACE, bad
+    for over in (X, R, W, S, H):
+        assert _linear(lib, **kw, ws=over) == INVALID
+    assert _linear(lib, **kw, bias=ws) == INVALID
 
 
 def test_valid_arguments_reach_the_device_check(built_library):
