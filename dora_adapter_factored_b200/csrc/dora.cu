@@ -713,6 +713,23 @@ bool layout_group(const int64_t* d_out, const int64_t* d_in, const int64_t* r, i
   return true;
 }
 
+template <typename O>
+cudaError_t linear_smem_attrs() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto kernel, int bytes) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  set(tile_i8_kernel<O, 1>, kTileI8MaxDynSmem);
+  set(tile_i8_kernel<O, 2>, kTileI8MaxDynSmem);
+  set(tile_i8_kernel<O, 4>, kTileI8MaxDynSmem);
+  set(tile_i8_kernel<O, 8>, kTileI8MaxDynSmem);
+  set(pair_i8_kernel<O, 1>, kPairI8MaxDynSmem);
+  set(pair_i8_kernel<O, 2>, kPairI8MaxDynSmem);
+  set(pair_i8_kernel<O, 4>, kPairI8MaxDynSmem);
+  return e;
+}
+
 bool ensure_tc_attrs() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
@@ -728,11 +745,8 @@ bool ensure_tc_attrs() {
           cudaSuccess ||
       (e = cudaFuncSetAttribute(merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kMaxDynSmem)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(tile_i8_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kTileI8MaxDynSmem)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(tile_i8_kernel<__nv_bfloat16>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kTileI8MaxDynSmem)) != cudaSuccess) {
+      (e = linear_smem_attrs<float>()) != cudaSuccess ||
+      (e = linear_smem_attrs<__nv_bfloat16>()) != cudaSuccess) {
     note_error("cudaFuncSetAttribute", e);
     return false;
   }
@@ -2129,55 +2143,115 @@ size_t tmem_smem_floor(uint32_t cols) {
   return std::max<size_t>(cols * kSmemPerTmemCol - 1024, size_t(64) << 10);
 }
 
-struct TileI8Plan {
-  int n, tiles_m, tiles_n, splits, stages, kb;
-  uint32_t cols;
-  size_t smem;
+// How the tensor-core path runs a shape: single CTAs or pairs, tokens per
+// tile, CTAs (pairs) that share a tile's k.
+struct LinearPlan {
+  bool pair;
+  int n, tiles_m, tiles_n, splits, kb;
 };
 
-TileI8Plan plan_tile_i8(int T, int d_out, int d_in, int sms) {
-  TileI8Plan p;
-  p.tiles_n = static_cast<int>(ceil_div_ll(T, kTileI8MaxN));
-  p.n = round_up_int(static_cast<int>(ceil_div_ll(T, p.tiles_n)), 16);
-  p.tiles_m = static_cast<int>(ceil_div_ll(d_out, kTileI8M));
-  p.kb = static_cast<int>(ceil_div_ll(d_in, kTileI8K));
+LinearPlan plan_linear(int T, int d_out, int d_in, int sms) {
+  LinearPlan p;
+  p.pair = T > 64;
+  p.tiles_n = static_cast<int>(ceil_div_ll(T, kI8MaxN));
+  p.n = round_up_int(static_cast<int>(ceil_div_ll(T, p.tiles_n)), p.pair ? 32 : 16);
+  p.tiles_m = static_cast<int>(ceil_div_ll(d_out, p.pair ? 2 * kI8M : kI8M));
+  p.kb = static_cast<int>(ceil_div_ll(d_in, kI8K));
   const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+  const int units = p.pair ? sms / 2 : sms;
   p.splits = 1;
-  while (p.splits < 8 && tiles * p.splits * 2 <= sms && p.kb >= p.splits * 2 * 4) p.splits *= 2;
-  p.cols = 32;
-  while (p.cols < static_cast<uint32_t>(p.n)) p.cols *= 2;
-  // Two CTAs per SM where there are more CTAs than SMs, else one.
-  const size_t stat = 232448 - kTileI8MaxDynSmem;  // the static part
-  const size_t tail = stat + 1024;                 // and the ring's alignment
-  const size_t budget = (tiles * p.splits > sms ? size_t(113) << 10 : size_t(kMaxDynSmem)) - tail;
-  const size_t stage = kTileI8WBytes + static_cast<size_t>(p.n) * kTileI8K;
-  const int kb_cta = static_cast<int>(ceil_div_ll(p.kb, p.splits));
-  p.stages = static_cast<int>(
-      std::min<size_t>({budget / stage, size_t(kTileI8MaxStages), static_cast<size_t>(kb_cta)}));
-  size_t ring = p.stages * stage;
-  if (p.splits > 1) ring = std::max(ring, static_cast<size_t>(p.n) * kTileI8M * 4);
-  p.smem = std::max(ring + 1024, tmem_smem_floor(p.cols) - sizeof(TileI8Tail));
+  while (p.splits < (p.pair ? 4 : 8) && tiles * p.splits * 2 <= units &&
+         p.kb >= p.splits * 2 * 4)
+    p.splits *= 2;
+  if (p.splits == 8) p.n = round_up_int(p.n, 32);  // n / splits in steps of four columns
   return p;
 }
 
 template <typename O>
-dora_status_t launch_tile_i8(const LinearArgs& A, const int8_t* xq, const int8_t* wq, int ld,
-                             int sms, cudaStream_t cs) {
-  const TileI8Plan p = plan_tile_i8(A.T, A.d_out, A.d_in, sms);
+dora_status_t launch_tile_i8(const LinearPlan& p, const LinearArgs& A, const int8_t* xq,
+                             const int8_t* wq, int ld, int sms, cudaStream_t cs) {
   static thread_local TileI8Dev P;
-  if (!make_tmap_i8(&P.tm_w, wq, A.d_out, ld, ld, kTileI8K, kTileI8M) ||
-      !make_tmap_i8(&P.tm_x, xq, A.T, ld, ld, kTileI8K, p.n))
+  if (!make_tmap_i8(&P.tm_w, wq, A.d_out, ld, ld, kI8K, kI8M) ||
+      !make_tmap_i8(&P.tm_x, xq, A.T, ld, ld, kI8K, p.n))
     return DORA_ERR_INVALID_ARG;
   P.a = A;
   P.n = p.n;
   P.kb = p.kb;
-  P.splits = p.splits;
-  P.stages = p.stages;
-  P.tmem_cols = p.cols;
-  P.idesc = idesc_i8_s32(kTileI8M, p.n);
-  launch_cluster(tile_i8_kernel<O>, dim3(p.tiles_m * p.splits, p.tiles_n), dim3(kTileI8Threads),
-                 p.smem, p.splits, cs, P, g_timeout_ns.load());
+  P.tmem_cols = 32;
+  while (P.tmem_cols < static_cast<uint32_t>(p.n)) P.tmem_cols *= 2;
+  P.idesc = idesc_i8_s32(kI8M, p.n);
+  // Two CTAs per SM where there are more CTAs than SMs, else one.  The
+  // partials of a split k lie behind the ring up to 32 KiB, else over it.
+  const long long ctas = static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits;
+  const size_t dyn = ctas > sms ? (size_t(113) << 10) - sizeof(TileI8Tail) : kTileI8MaxDynSmem;
+  const size_t part = i8_partial_bytes(p.n, p.splits);
+  P.part_over_ring = part > (size_t(32) << 10);
+  const size_t stage = kI8WBytes + static_cast<size_t>(p.n) * kI8K;
+  const size_t room = dyn - 1024 - (P.part_over_ring ? 0 : part);
+  P.stages = static_cast<int>(std::min<size_t>(
+      {room / stage, size_t(kI8MaxStages), static_cast<size_t>(ceil_div_ll(p.kb, p.splits))}));
+  const size_t ring = P.stages * stage;
+  P.part_off = P.part_over_ring ? 0 : static_cast<uint32_t>(ring);
+  const size_t used = P.part_over_ring ? std::max(ring, part) : ring + part;
+  const size_t smem = std::max(used + 1024, tmem_smem_floor(P.tmem_cols) - sizeof(TileI8Tail));
+  const dim3 grid(p.tiles_m * p.splits, p.tiles_n);
+  const unsigned long long to = g_timeout_ns.load();
+  auto go = [&](auto kernel) {
+    launch_cluster(kernel, grid, dim3(kTileI8Threads), smem, p.splits, cs, P, to);
+  };
+  switch (p.splits) {
+    case 1: go(tile_i8_kernel<O, 1>); break;
+    case 2: go(tile_i8_kernel<O, 2>); break;
+    case 4: go(tile_i8_kernel<O, 4>); break;
+    default: go(tile_i8_kernel<O, 8>); break;
+  }
   return launch_status();
+}
+
+// Token tiles that go together: their codes stay in L2 while the weight
+// streams past.
+constexpr size_t kPairI8GroupBytes = size_t(32) << 20;
+
+template <typename O>
+dora_status_t launch_pair_i8(const LinearPlan& p, const LinearArgs& A, const int8_t* xq,
+                             const int8_t* wq, int ld, int sms, cudaStream_t cs) {
+  static thread_local PairI8Dev P;
+  if (!make_tmap_i8(&P.tm_w, wq, A.d_out, ld, ld, kI8K, kI8M) ||
+      !make_tmap_i8(&P.tm_x, xq, A.T, ld, ld, kI8K, p.n / 2))
+    return DORA_ERR_INVALID_ARG;
+  P.a = A;
+  P.n = p.n;
+  P.kb = p.kb;
+  P.tiles_m = p.tiles_m;
+  P.tiles_n = p.tiles_n;
+  P.group = static_cast<int>(std::max<size_t>(
+      1, std::min<size_t>(p.tiles_n, kPairI8GroupBytes / (static_cast<size_t>(p.n) * ld))));
+  P.idesc = idesc_i8_s32(2 * kI8M, p.n);
+  const size_t stage = kI8WBytes + static_cast<size_t>(p.n / 2) * kI8K;
+  P.stages = static_cast<int>(
+      std::min<size_t>((kPairI8MaxDynSmem - 1024) / stage, size_t(kI8MaxStages)));
+  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+  const long long clusters = p.splits > 1 ? tiles : std::min<long long>(tiles, sms / 2);
+  const unsigned long long to = g_timeout_ns.load();
+  // All of an SM's shared memory, as all of its TMEM.
+  auto go = [&](auto kernel) {
+    launch_cluster(kernel, dim3(static_cast<unsigned>(clusters * 2 * p.splits)),
+                   dim3(kPairI8Threads), kPairI8MaxDynSmem, 2 * p.splits, cs, P, to);
+  };
+  switch (p.splits) {
+    case 1: go(pair_i8_kernel<O, 1>); break;
+    case 2: go(pair_i8_kernel<O, 2>); break;
+    default: go(pair_i8_kernel<O, 4>); break;
+  }
+  return launch_status();
+}
+
+template <typename O>
+dora_status_t launch_tensor_i8(const LinearArgs& A, const int8_t* xq, const int8_t* wq, int ld,
+                               int sms, cudaStream_t cs) {
+  const LinearPlan p = plan_linear(A.T, A.d_out, A.d_in, sms);
+  return p.pair ? launch_pair_i8<O>(p, A, xq, wq, ld, sms, cs)
+                : launch_tile_i8<O>(p, A, xq, wq, ld, sms, cs);
 }
 
 template <typename O>
@@ -2191,7 +2265,7 @@ dora_status_t launch_linear(const LinearArgs& A, void* ws, int sms, cudaStream_t
     launch_dot_any<O>(A, vec, sms, cs);
     return launch_status();
   }
-  if (!pads) return launch_tile_i8<O>(A, A.xq, A.wq, A.d_in, sms, cs);
+  if (!pads) return launch_tensor_i8<O>(A, A.xq, A.wq, A.d_in, sms, cs);
   const int ld = padded_k(A.d_in);
   int8_t* xp = static_cast<int8_t*>(ws);
   int8_t* wp = xp + linear_pad_x(A.T, A.d_in);
@@ -2201,7 +2275,7 @@ dora_status_t launch_linear(const LinearArgs& A, void* ws, int sms, cudaStream_t
       std::min<long long>(ceil_div_ll(chunks, kPadThreads), 8ll * sms));
   launch_stream(pad_rows_kernel, dim3(gx, 2), dim3(kPadThreads), 0, cs, px, pw);
   const dora_status_t st = launch_status();
-  return st != DORA_OK ? st : launch_tile_i8<O>(A, xp, wp, ld, sms, cs);
+  return st != DORA_OK ? st : launch_tensor_i8<O>(A, xp, wp, ld, sms, cs);
 }
 }  // namespace
 }  // namespace dora

@@ -145,39 +145,126 @@ __global__ void __launch_bounds__(kDotWarps * 32) dot_i8_kernel(const LinearArgs
 }
 
 // ---------------------------------------------------------- tensor cores
-// One tile of 128 output channels by up to 256 tokens per CTA: the weight's
-// rows are the MMA's M, the tokens its N (so that a small batch wastes no
-// rows, and the epilogue's lanes are consecutive channels of y).  TMA brings
-// k-blocks of 128 codes of both operands into a ring of 128-byte-swizzled
-// stages; one thread issues the MMAs into an int32 accumulator in TMEM.
-// `splits` CTAs of a cluster share a tile's k where the tiles alone would
-// leave SMs idle: each leaves its partial in shared memory and takes a share
-// of the columns, summed over the cluster's shared memory (int32, exact in any
-// order).  Not persistent: with up to 113 KiB and 256 TMEM columns per CTA two
-// CTAs share an SM, so one's epilogue runs beside the other's stream.
-constexpr int kTileI8M = 128;
-constexpr int kTileI8K = 128;  // codes per k-block: one 128-byte swizzle row
-constexpr int kTileI8MaxN = 256;
+// The weight's rows are the MMA's M and the tokens its N, so that a small
+// batch wastes no rows and the lanes of an epilogue warp are consecutive
+// channels of y.  TMA brings k-blocks of 128 codes of both operands into a
+// ring of 128-byte-swizzled stages; one thread issues the MMAs into an int32
+// accumulator in TMEM (lane = channel, column = token).
+//
+// Where the tiles alone would leave SMs idle, S CTAs (or pairs) of a cluster
+// share a tile's k.  Each finishes n / S of the tile's columns: the others
+// push their partials of those columns into its shared memory, each thread
+// four columns of its channel per store (scalar stores, or pulling the
+// partials, cost the remote latency or the address arithmetic per column).
+constexpr int kI8M = 128;  // channels per CTA (TMEM lanes)
+constexpr int kI8K = 128;  // codes per k-block: one 128-byte swizzle row
+constexpr int kI8MaxN = 256;
+constexpr int kI8MaxStages = 12;
+constexpr uint32_t kI8WBytes = kI8M * kI8K;  // 16 KiB of weight per stage and CTA
+
+__device__ __forceinline__ void linear_give_up(volatile int* abort_flag) {
+  *abort_flag = 1;
+  record_error(DORA_ERR_TIMEOUT);
+}
+
+// This thread's channel of y: what its columns are scaled and stored with.
+template <typename O>
+struct ChannelOut {
+  O* y;  // column 0 of the channel
+  float sw, bias;
+  bool ok, has_bias;
+  int T;
+  long long d_out;
+  __device__ __forceinline__ ChannelOut(const LinearArgs& a, int row, bool may_store) {
+    ok = may_store && row < a.d_out && DORA_BOUNDS_OK(row >= 0);
+    has_bias = a.bias != nullptr;
+    y = static_cast<O*>(a.y) + row;
+    sw = ok ? a.w_scale[row] : 0.f;
+    bias = ok && has_bias ? a.bias[row] : 0.f;
+    T = a.T;
+    d_out = a.d_out;
+  }
+  __device__ __forceinline__ void put(int t, int acc, float sx) const {
+    if (ok && t < T) linear_store(y + t * d_out, linear_value(acc, sx, sw, bias, has_bias));
+  }
+};
+
+// Partials of a split k in a CTA: [S][128 channels][n / S columns, padded by
+// one 16-byte step against bank conflicts] int32.
+__host__ __device__ constexpr uint32_t i8_partial_stride(int n, int S) { return n / S + 4; }
+__host__ __device__ constexpr uint32_t i8_partial_bytes(int n, int S) {
+  return S > 1 ? static_cast<uint32_t>(S) * kI8M * i8_partial_stride(n, S) * 4u : 0u;
+}
+
+// Threads 0-127: pushes this CTA's accumulator columns to the CTAs that finish
+// them.  `slice`: this CTA's share of k; the CTA of slice s has cluster rank
+// s * rank_step + rank_off.  n is a multiple of 16 and n / S of 4.
+template <int S>
+__device__ __forceinline__ void i8_push_partials(uint32_t lane_base, int n, int slice,
+                                                 int rank_step, int rank_off, const int* part) {
+  const int cols = n / S;
+  const uint32_t stride = i8_partial_stride(n, S);
+  const uint32_t mine =
+      smem_addr(part) + (static_cast<uint32_t>(slice) * kI8M + threadIdx.x) * stride * 4u;
+  for (int c0 = 0; c0 < n; c0 += 16) {
+    int v[16];
+    tmem_load_16cols(lane_base + c0, v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = c0 + 4 * q, owner = c / cols;
+      st_cluster_v4(mapa_shared(mine + static_cast<uint32_t>(c - owner * cols) * 4u,
+                                static_cast<uint32_t>(owner * rank_step + rank_off)),
+                    v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    }
+    __syncwarp();
+  }
+}
+
+// Threads 0-127: sums and stores this CTA's columns of the tile at token t0.
+template <int S, typename O>
+__device__ __forceinline__ void i8_finish_columns(const ChannelOut<O>& out, const float* sx, int n,
+                                                  int slice, int t0, const int* part) {
+  const int cols = n / S;
+  const uint32_t stride = i8_partial_stride(n, S);
+  for (int c = 0; c < cols; c += 4) {
+    int4 sum = make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int4 v =
+          *reinterpret_cast<const int4*>(part + (s * kI8M + threadIdx.x) * stride + c);
+      sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+    }
+    const int at = slice * cols + c;
+    out.put(t0 + at, sum.x, sx[at]);
+    out.put(t0 + at + 1, sum.y, sx[at + 1]);
+    out.put(t0 + at + 2, sum.z, sx[at + 2]);
+    out.put(t0 + at + 3, sum.w, sx[at + 3]);
+  }
+}
+
+// ------------------------------------------------ single CTAs: small batches
+// One tile of 128 channels by up to 256 tokens per CTA.  Not persistent: with
+// up to 113 KiB and 256 TMEM columns per CTA two CTAs share an SM, so one's
+// epilogue runs beside the other's stream.
 constexpr int kTileI8Threads = 128;
-constexpr int kTileI8MaxStages = 12;
-constexpr uint32_t kTileI8WBytes = kTileI8M * kTileI8K;  // 16 KiB of weight per stage
 
 struct alignas(64) TileI8Dev {
   CUtensorMap tm_w;  // wq [d_out, ld], box 128 x 128
   CUtensorMap tm_x;  // xq [T, ld],     box 128 x n
   LinearArgs a;
-  int n;             // tokens per tile, a multiple of 16
+  int n;             // tokens per tile
   int kb;            // k-blocks
-  int splits;
   int stages;
+  uint32_t part_off; // of the partials, from the ring's start
+  int part_over_ring;
   uint32_t tmem_cols, idesc;
 };
 
 struct TileI8Tail {
-  uint64_t full[kTileI8MaxStages];
-  uint64_t empty[kTileI8MaxStages];
+  uint64_t full[kI8MaxStages];
+  uint64_t empty[kI8MaxStages];
   uint64_t acc;
-  float sx[kTileI8MaxN];
+  float sx[kI8MaxN];
   uint32_t tmem_slot;
   int abort_flag;
 };
@@ -185,12 +272,7 @@ struct TileI8Tail {
 // Dynamic shared memory a CTA may ask for beside the static TileI8Tail.
 constexpr int kTileI8MaxDynSmem = 232448 - static_cast<int>(sizeof(TileI8Tail) + 127) / 128 * 128;
 
-__device__ __forceinline__ void tile_give_up(volatile int* abort_flag) {
-  *abort_flag = 1;
-  record_error(DORA_ERR_TIMEOUT);
-}
-
-template <typename O>
+template <typename O, int S>
 __global__ void __launch_bounds__(kTileI8Threads)
     tile_i8_kernel(const __grid_constant__ TileI8Dev P, unsigned long long timeout_ns) {
   extern __shared__ uint8_t smem_raw[];
@@ -199,12 +281,12 @@ __global__ void __launch_bounds__(kTileI8Threads)
   __shared__ TileI8Tail tail;
   volatile int* abort_flag = &tail.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slice = static_cast<int>(blockIdx.x) % P.splits;  // = rank in the cluster
-  const int row0 = static_cast<int>(blockIdx.x) / P.splits * kTileI8M;
+  const int slice = static_cast<int>(blockIdx.x) % S;  // = rank in the cluster
+  const int row0 = static_cast<int>(blockIdx.x) / S * kI8M;
   const int t0 = static_cast<int>(blockIdx.y) * P.n;
-  const int kb0 = static_cast<int>(static_cast<long long>(slice) * P.kb / P.splits);
-  const int kb1 = static_cast<int>(static_cast<long long>(slice + 1) * P.kb / P.splits);
-  const uint32_t stage_bytes = kTileI8WBytes + static_cast<uint32_t>(P.n) * kTileI8K;
+  const int kb0 = static_cast<int>(static_cast<long long>(slice) * P.kb / S);
+  const int kb1 = static_cast<int>(static_cast<long long>(slice + 1) * P.kb / S);
+  const uint32_t stage_bytes = kI8WBytes + static_cast<uint32_t>(P.n) * kI8K;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < P.stages; ++s) {
@@ -222,7 +304,10 @@ __global__ void __launch_bounds__(kTileI8Threads)
     tmem_relinquish();
   }
   tc_fence_before_sync();
-  __syncthreads();
+  if constexpr (S > 1)
+    cluster_sync();  // the other CTAs run: their shared memory may be written
+  else
+    __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = tail.tmem_slot;
   grid_dependency_wait();
@@ -235,13 +320,13 @@ __global__ void __launch_bounds__(kTileI8Threads)
       uint32_t phase = 0;
       for (int k = kb0; k < kb1; ++k) {
         if (!mbar_wait(&tail.empty[stage], phase ^ 1u, timeout_ns, abort_flag)) {
-          tile_give_up(abort_flag);
+          linear_give_up(abort_flag);
           break;
         }
         uint8_t* st = ring + stage * stage_bytes;
         mbar_arrive_expect_tx(&tail.full[stage], stage_bytes);
-        tma_load_2d(st, &P.tm_w, &tail.full[stage], k * kTileI8K, row0, pol_w);
-        tma_load_2d(st + kTileI8WBytes, &P.tm_x, &tail.full[stage], k * kTileI8K, t0, pol_x);
+        tma_load_2d(st, &P.tm_w, &tail.full[stage], k * kI8K, row0, pol_w);
+        tma_load_2d(st + kI8WBytes, &P.tm_x, &tail.full[stage], k * kI8K, t0, pol_x);
         ++issued;
         if (++stage == P.stages) {
           stage = 0;
@@ -259,13 +344,13 @@ __global__ void __launch_bounds__(kTileI8Threads)
       uint32_t phase = 0;
       for (int k = kb0; k < kb1; ++k) {
         if (!mbar_wait(&tail.full[stage], phase, timeout_ns, abort_flag)) {
-          tile_give_up(abort_flag);
+          linear_give_up(abort_flag);
           break;
         }
         tc_fence_after_sync();
-        const uint32_t w = smem_addr(ring + stage * stage_bytes), x = w + kTileI8WBytes;
+        const uint32_t w = smem_addr(ring + stage * stage_bytes), x = w + kI8WBytes;
 #pragma unroll
-        for (int kk = 0; kk < kTileI8K / 32; ++kk)
+        for (int kk = 0; kk < kI8K / 32; ++kk)
           umma_i8(tmem, sw128_kmajor_desc(w + kk * 32), sw128_kmajor_desc(x + kk * 32), P.idesc,
                   (k > kb0 || kk > 0) ? 1u : 0u);
         umma_commit(&tail.empty[stage]);
@@ -282,60 +367,294 @@ __global__ void __launch_bounds__(kTileI8Threads)
       tail.sx[c] = t0 + c < P.a.T ? P.a.x_scale[t0 + c] : 0.f;
   }
   __syncwarp();
-  const int row = row0 + static_cast<int>(threadIdx.x);  // TMEM lane = channel of the tile
-  const bool has_bias = P.a.bias != nullptr;
-  const bool row_ok = row < P.a.d_out;
-  const float sw = row_ok ? P.a.w_scale[row] : 0.f;
-  const float bias = row_ok && has_bias ? P.a.bias[row] : 0.f;
-  if (!mbar_wait(&tail.acc, 0, timeout_ns, abort_flag)) tile_give_up(abort_flag);
+  if (!mbar_wait(&tail.acc, 0, timeout_ns, abort_flag)) linear_give_up(abort_flag);
   __syncthreads();  // every wait is over, sx is written
   tc_fence_after_sync();
-  const bool ok = *abort_flag == 0;
+  const ChannelOut<O> out(P.a, row0 + static_cast<int>(threadIdx.x), *abort_flag == 0);
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-  O* y = static_cast<O*>(P.a.y);
-  if (P.splits == 1) {
+  if constexpr (S == 1) {
     for (int c0 = 0; c0 < P.n; c0 += 16) {
       int v[16];
       tmem_load_16cols(lane_base + c0, v);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const int t = t0 + c0 + c;
-        if (ok && row_ok && t < P.a.T && DORA_BOUNDS_OK(row >= 0 && t >= 0))
-          linear_store(y + static_cast<size_t>(t) * P.a.d_out + row,
-                       linear_value(v[c], tail.sx[c0 + c], sw, bias, has_bias));
-      }
+      for (int c = 0; c < 16; ++c) out.put(t0 + c0 + c, v[c], tail.sx[c0 + c]);
       __syncwarp();
     }
   } else {
-    // The ring is free: its copies have landed and its MMAs have completed.
-    int* part = reinterpret_cast<int*>(ring);  // [n][128]
-    for (int c0 = 0; c0 < P.n; c0 += 16) {
-      int v[16];
-      tmem_load_16cols(lane_base + c0, v);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) part[(c0 + c) * kTileI8M + threadIdx.x] = v[c];
+    // Behind the ring, or over it once every CTA's copies have landed and its
+    // MMAs have completed.
+    if (P.part_over_ring) {
+      __syncwarp();
+      cluster_sync();
     }
-    __syncwarp();
+    const int* part = reinterpret_cast<const int*>(ring + P.part_off);
+    i8_push_partials<S>(lane_base, P.n, slice, 1, 0, part);
     cluster_sync();
-    const uint32_t mine = smem_addr(part) + threadIdx.x * 4;
-    for (int c = slice; c < P.n && t0 + c < P.a.T; c += P.splits) {
-      int sum = 0;
-      for (int s = 0; s < P.splits; ++s)
-        sum += ld_cluster_s32(
-            mapa_shared(mine + static_cast<uint32_t>(c * kTileI8M * 4), static_cast<uint32_t>(s)));
-      const int t = t0 + c;
-      if (ok && row_ok && DORA_BOUNDS_OK(row >= 0 && t < P.a.T))
-        linear_store(y + static_cast<size_t>(t) * P.a.d_out + row,
-                     linear_value(sum, tail.sx[c], sw, bias, has_bias));
-    }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while another reads its partial
+    i8_finish_columns<S>(out, tail.sx, P.n, slice, t0, part);
   }
   tc_fence_before_sync();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, P.tmem_cols);
+  }
+}
+
+// ------------------------------------------------------- CTA pairs: the rest
+// Tiles of 256 channels by n tokens on CTA pairs (one MMA of M = 256 for both,
+// issued by rank 0 of the pair): each CTA stages its 128 rows of the weight
+// and half of the tokens, 32 KiB per k-block at n = 256 where a CTA alone
+// stages 48 for half the work.  At the 8-bit rate a k-block lasts 512 cycles,
+// in which its bytes cross shared memory twice (copied in, read by the MMA):
+// 128 bytes a cycle, what shared memory moves, against 192 on single CTAs.
+// S == 1: persistent, over all tiles, with two accumulators of 256 columns so
+// that a tile's epilogue runs beside the next one's MMAs.  S > 1: one tile per
+// cluster of S pairs, which share its k.
+constexpr int kPairI8EpiWarps = 4;
+constexpr int kPairI8Threads = (kPairI8EpiWarps + 2) * 32;  // + copies, + MMA
+
+struct alignas(64) PairI8Dev {
+  CUtensorMap tm_w;  // wq [d_out, ld], box 128 x 128
+  CUtensorMap tm_x;  // xq [T, ld],     box 128 x n / 2
+  LinearArgs a;
+  int n;             // tokens per tile, a multiple of 32
+  int kb;            // k-blocks
+  int stages;
+  int tiles_m, tiles_n, group;  // `group` token tiles go together, channels outside
+  uint32_t idesc;
+};
+
+// Barriers (per CTA, same offsets in both CTAs of a pair):
+//   full[s]       rank 0: its producer's expected bytes plus both CTAs' copies.
+//   empty[s]      both: rank 0's commit after the MMAs reading stage s.
+//   acc_full[b]   both: rank 0's commit after a tile's MMAs into accumulator b.
+//   acc_empty[b]  rank 0: one arrival per epilogue warp of both CTAs.
+//   drain         rank 0: the last MMAs have completed.
+struct PairI8Tail {
+  uint64_t full[kI8MaxStages];
+  uint64_t empty[kI8MaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  float sx[kPairI8EpiWarps][kI8MaxN];  // a tile's token scales, per epilogue warp
+  uint32_t tmem_slot;
+  int abort_flag;
+};
+
+constexpr int kPairI8MaxDynSmem = 232448 - static_cast<int>(sizeof(PairI8Tail) + 127) / 128 * 128;
+
+// Token tile and channel tile of the i-th tile: groups of token tiles, inside
+// a group all its token tiles of one channel tile before the next, so that the
+// weight is streamed once per group and the group's tokens stay in L2.
+__device__ __forceinline__ void pair_tile(const PairI8Dev& P, int i, int& tm, int& tn) {
+  const int per_group = P.group * P.tiles_m;
+  const int g = i / per_group, j = i - g * per_group;
+  const int width = min(P.group, P.tiles_n - g * P.group);
+  tm = j / width;
+  tn = g * P.group + j - tm * width;
+}
+
+template <typename O, int S>
+__global__ void __launch_bounds__(kPairI8Threads)
+    pair_i8_kernel(const __grid_constant__ PairI8Dev P, unsigned long long timeout_ns) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  __shared__ PairI8Tail tail;
+  volatile int* abort_flag = &tail.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank(), half = rank & 1u, lead = rank & ~1u;
+  const int slice = static_cast<int>(rank >> 1);
+  const uint32_t peer_abort = mapa_shared(smem_addr(&tail.abort_flag), rank ^ 1u);
+  const int kb0 = static_cast<int>(static_cast<long long>(slice) * P.kb / S);
+  const int kb1 = static_cast<int>(static_cast<long long>(slice + 1) * P.kb / S);
+  const uint32_t stage_bytes = kI8WBytes + static_cast<uint32_t>(P.n / 2) * kI8K;
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
+  const int tiles = P.tiles_m * P.tiles_n;
+  const int first = static_cast<int>(blockIdx.x) / (2 * S);
+  const int step = static_cast<int>(gridDim.x) / (2 * S);
+  auto give_up = [&] {
+    st_cluster_u32(peer_abort, 1u);
+    linear_give_up(abort_flag);
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P.stages; ++s) {
+      mbar_init(&tail.full[s], 1);
+      mbar_init(&tail.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tail.acc_full[b], 1);
+      mbar_init(&tail.acc_empty[b], 2 * kPairI8EpiWarps);
+    }
+    mbar_init(&tail.drain, 1);
+    tail.abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&P.tm_w);
+    prefetch_tmap(&P.tm_x);
+  }
+  if (warp == 0) {
+    tmem_alloc_pair(&tail.tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  // Both CTAs' barriers are initialised before either signals the other.
+  tc_fence_before_sync();
+  cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = tail.tmem_slot;
+  grid_dependency_wait();
+  grid_dependency_trigger();  // not before TMEM is held: the next grid may want it too
+
+  if (warp == kPairI8EpiWarps) {
+    // ---------------------------------------------------------- copy producer
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last();
+      const uint32_t full0 = mapa_shared(smem_addr(&tail.full[0]), lead);
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int i = first; ok && i < tiles; i += step) {
+        int tm, tn;
+        pair_tile(P, i, tm, tn);
+        const int row = tm * 2 * kI8M + static_cast<int>(half) * kI8M;
+        const int tok = tn * P.n + static_cast<int>(half) * (P.n / 2);
+        for (int k = kb0; k < kb1; ++k) {
+          if (!mbar_wait(&tail.empty[stage], phase ^ 1u, timeout_ns, abort_flag)) {
+            give_up();
+            ok = false;
+            break;
+          }
+          uint8_t* st = ring + stage * stage_bytes;
+          const uint32_t bar = full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
+          if (half == 0) mbar_arrive_expect_tx(&tail.full[stage], 2 * stage_bytes);
+          tma_load_2d_pair(st, &P.tm_w, bar, k * kI8K, row, pol);
+          tma_load_2d_pair(st + kI8WBytes, &P.tm_x, bar, k * kI8K, tok, pol);
+          ++issued;
+          if (++stage == P.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Every copy lands before the CTA can exit: rank 0 sees its full
+      // barriers complete; rank 1's copies complete on those, so it waits for
+      // its stages to be consumed.
+      for (long long j = issued > P.stages ? issued - P.stages : 0; j < issued; ++j) {
+        const uint32_t par = static_cast<uint32_t>((j / P.stages) & 1);
+        mbar_wait(half == 0 ? &tail.full[j % P.stages] : &tail.empty[j % P.stages], par,
+                  kDrainTimeoutNs, nullptr);
+      }
+    }
+  } else if (warp == kPairI8EpiWarps + 1) {
+    // ------------------------------------------------------------- MMA issuer
+    if (lane == 0 && half == 0) {
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = first; ok && i < tiles; i += step, ++it) {
+        const int b = it & 1;
+        if (!mbar_wait(&tail.acc_empty[b], static_cast<uint32_t>(((it >> 1) & 1) ^ 1), timeout_ns,
+                       abort_flag)) {
+          give_up();
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d = tmem + static_cast<uint32_t>(b * kI8MaxN);
+        for (int k = kb0; k < kb1; ++k) {
+          if (!mbar_wait(&tail.full[stage], phase, timeout_ns, abort_flag)) {
+            give_up();
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t w = smem_addr(ring + stage * stage_bytes), x = w + kI8WBytes;
+#pragma unroll
+          for (int kk = 0; kk < kI8K / 32; ++kk)
+            umma_i8_pair(d, sw128_kmajor_desc(w + kk * 32), sw128_kmajor_desc(x + kk * 32),
+                         P.idesc, (k > kb0 || kk > 0) ? 1u : 0u);
+          umma_commit_pair(&tail.empty[stage], pair_mask);
+          if (++stage == P.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        umma_commit_pair(&tail.acc_full[b], pair_mask);
+      }
+      // Also after a give-up: no MMA is in flight when the CTAs leave.
+      umma_commit_pair(&tail.drain, static_cast<uint16_t>(1u << lead));
+      mbar_wait(&tail.drain, 0, kDrainTimeoutNs, nullptr);
+    }
+  } else {
+    // ---------------------------------------------------- epilogue (warps 0-3)
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t empty0 = mapa_shared(smem_addr(&tail.acc_empty[0]), lead);
+    float* sx = tail.sx[S == 1 ? warp : 0];
+    int it = 0;
+    for (int i = first; i < tiles; i += step, ++it) {
+      int tm, tn;
+      pair_tile(P, i, tm, tn);
+      const int b = it & 1, t0 = tn * P.n;
+      const int row = tm * 2 * kI8M + static_cast<int>(half) * kI8M + warp * 32 + lane;
+      // Each warp its own copy of the scales (S == 1), or one for the CTA.
+      for (int c = S == 1 ? lane : static_cast<int>(threadIdx.x); c < P.n; c += S == 1 ? 32 : 128)
+        sx[c] = t0 + c < P.a.T ? P.a.x_scale[t0 + c] : 0.f;
+      __syncwarp();
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(&tail.acc_full[b], static_cast<uint32_t>((it >> 1) & 1),
+                                timeout_ns, abort_flag))) {
+        give_up();
+        break;
+      }
+      tc_fence_after_sync();
+      if constexpr (S == 1) {
+        const ChannelOut<O> out(P.a, row, *abort_flag == 0);
+        const uint32_t acc = lane_base + static_cast<uint32_t>(b * kI8MaxN);
+        for (int c0 = 0; c0 < P.n; c0 += 16) {
+          int v[16];
+          tmem_load_16cols(acc + c0, v);
+          if (c0 + 16 >= P.n) {  // the accumulator is in registers: hand it back
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+              mbar_arrive_cluster_relaxed(empty0 + b * static_cast<uint32_t>(sizeof(uint64_t)));
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) out.put(t0 + c0 + c, v[c], sx[c0 + c]);
+          __syncwarp();
+        }
+      }
+    }
+  }
+  if constexpr (S > 1) {
+    // The one tile's partials, over the ring: no copy or MMA of any CTA of the
+    // cluster is in flight past the first barrier.
+    int tm, tn;
+    pair_tile(P, first, tm, tn);
+    const int t0 = tn * P.n;
+    const int* part = reinterpret_cast<const int*>(ring);
+    __syncwarp();
+    tc_fence_before_sync();
+    cluster_sync();
+    tc_fence_after_sync();
+    if (warp < kPairI8EpiWarps)
+      i8_push_partials<S>(tmem + (static_cast<uint32_t>(warp * 32) << 16), P.n, slice, 2,
+                          static_cast<int>(half), part);
+    __syncwarp();
+    cluster_sync();
+    if (warp < kPairI8EpiWarps) {
+      const ChannelOut<O> out(P.a, tm * 2 * kI8M + static_cast<int>(half) * kI8M + threadIdx.x,
+                              *abort_flag == 0);
+      i8_finish_columns<S>(out, tail.sx[0], P.n, slice, t0, part);
+    }
+  }
+  // Neither CTA leaves (or frees TMEM) while the other may still signal it or
+  // read its shared memory through the MMAs.
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_sync();
+  if (warp == 0) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
