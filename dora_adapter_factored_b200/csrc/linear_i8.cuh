@@ -7,6 +7,8 @@
 // of y: a token's row is the same alone and in any batch.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "sm100.cuh"
 
@@ -168,26 +170,87 @@ __device__ __forceinline__ void linear_give_up(volatile int* abort_flag) {
 }
 
 // This thread's channel of y: what its columns are scaled and stored with.
+// All lanes of a warp call put together (its pairs of lanes exchange values).
 template <typename O>
 struct ChannelOut {
-  O* y;  // column 0 of the channel
+  O* y;  // the channel's column 0; where `pairs`, of the even channel of its pair
   float sw, bias;
   bool ok, has_bias;
+  bool pairs;  // bf16: channels 2i and 2i + 1 are stored together, 4 bytes aligned
   int T;
   long long d_out;
   __device__ __forceinline__ ChannelOut(const LinearArgs& a, int row, bool may_store) {
     ok = may_store && row < a.d_out && DORA_BOUNDS_OK(row >= 0);
     has_bias = a.bias != nullptr;
-    y = static_cast<O*>(a.y) + row;
+    pairs = sizeof(O) == 2 && a.d_out % 2 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 3) == 0;
+    y = static_cast<O*>(a.y) + (pairs ? row & ~1 : row);
     sw = ok ? a.w_scale[row] : 0.f;
     bias = ok && has_bias ? a.bias[row] : 0.f;
     T = a.T;
     d_out = a.d_out;
   }
-  __device__ __forceinline__ void put(int t, int acc, float sx) const {
-    if (ok && t < T) linear_store(y + t * d_out, linear_value(acc, sx, sw, bias, has_bias));
+  // N columns from token t.  Their scales (16-byte aligned in shared memory)
+  // are read before any is stored: a load between the stores would have to
+  // wait for them, since y might alias it.  bf16 values are rounded two to an
+  // instruction and stored by pairs of channels: the even lane of a pair
+  // stores both channels of one column, the odd lane those of the next (one
+  // 2-byte store and one rounding per value made the epilogue of 128 columns
+  // 5.1 us).
+  template <int N>
+  __device__ __forceinline__ void put(int t, const int (&acc)[N], const float* sx) const {
+    float s[N];
+#pragma unroll
+    for (int c = 0; c < N; c += 4)
+      *reinterpret_cast<float4*>(s + c) = *reinterpret_cast<const float4*>(sx + c);
+    O* p = y + t * d_out;
+    const int left = ok ? T - t : 0;
+    if constexpr (sizeof(O) == 2) {
+      const bool odd = threadIdx.x & 1;
+      if (pairs) p += odd ? d_out : 0;
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const uint32_t v =
+            pack_bf16x2_rn(linear_value(acc[c], s[c], sw, bias, has_bias),
+                           linear_value(acc[c + 1], s[c + 1], sw, bias, has_bias));
+        if (pairs) {
+          const uint32_t u = __shfl_xor_sync(0xffffffffu, v, 1);
+          if (c + (odd ? 1 : 0) < left)
+            *reinterpret_cast<uint32_t*>(p) =
+                odd ? __byte_perm(u, v, 0x7632) : __byte_perm(v, u, 0x5410);
+        } else {
+          uint16_t* h = reinterpret_cast<uint16_t*>(p);
+          if (c < left) h[0] = static_cast<uint16_t>(v);
+          if (c + 1 < left) h[d_out] = static_cast<uint16_t>(v >> 16);
+        }
+        p += 2 * d_out;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; ++c, p += d_out)
+        if (c < left) *p = linear_value(acc[c], s[c], sw, bias, has_bias);
+    }
   }
 };
+
+// Calls f(c, v) with the n accumulator columns (a multiple of 16) from `tmem`,
+// 16 at a time, the next 16 on their way meanwhile.
+template <typename F>
+__device__ __forceinline__ void for_columns(uint32_t tmem, int n, F&& f) {
+  int a[16], b[16];
+  tmem_load_16cols(tmem, a);
+  for (int c = 0; c < n; c += 32) {
+    tmem_wait_16cols(a);
+    if (c + 16 < n) tmem_load_16cols(tmem + c + 16, b);
+    f(c, a);
+    __syncwarp();
+    if (c + 16 < n) {
+      tmem_wait_16cols(b);
+      if (c + 32 < n) tmem_load_16cols(tmem + c + 32, a);
+      f(c + 16, b);
+      __syncwarp();
+    }
+  }
+}
 
 // Partials of a split k in a CTA: [S][128 channels][n / S columns, padded by
 // one 16-byte step against bank conflicts] int32.
@@ -206,18 +269,20 @@ __device__ __forceinline__ void i8_push_partials(uint32_t lane_base, int n, int 
   const uint32_t stride = i8_partial_stride(n, S);
   const uint32_t mine =
       smem_addr(part) + (static_cast<uint32_t>(slice) * kI8M + threadIdx.x) * stride * 4u;
-  for (int c0 = 0; c0 < n; c0 += 16) {
-    int v[16];
-    tmem_load_16cols(lane_base + c0, v);
+  int owner = 0, in = 0;  // of the next four columns
+  for_columns(lane_base, n, [&](int, const int(&v)[16]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = c0 + 4 * q, owner = c / cols;
-      st_cluster_v4(mapa_shared(mine + static_cast<uint32_t>(c - owner * cols) * 4u,
+    for (int q = 0; q < 16; q += 4) {
+      st_cluster_v4(mapa_shared(mine + static_cast<uint32_t>(in) * 4u,
                                 static_cast<uint32_t>(owner * rank_step + rank_off)),
-                    v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    v[q], v[q + 1], v[q + 2], v[q + 3]);
+      in += 4;
+      if (in == cols) {
+        in = 0;
+        ++owner;
+      }
     }
-    __syncwarp();
-  }
+  });
 }
 
 // Threads 0-127: sums and stores this CTA's columns of the tile at token t0.
@@ -225,21 +290,28 @@ template <int S, typename O>
 __device__ __forceinline__ void i8_finish_columns(const ChannelOut<O>& out, const float* sx, int n,
                                                   int slice, int t0, const int* part) {
   const int cols = n / S;
-  const uint32_t stride = i8_partial_stride(n, S);
-  for (int c = 0; c < cols; c += 4) {
-    int4 sum = make_int4(0, 0, 0, 0);
+  const int* p = part + threadIdx.x * i8_partial_stride(n, S);
+  const uint32_t from = kI8M * i8_partial_stride(n, S);  // to the next slice's partials
+  auto group = [&](auto width, int c) {
+    constexpr int N = decltype(width)::value;
+    int sum[N];
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int4 v =
-          *reinterpret_cast<const int4*>(part + (s * kI8M + threadIdx.x) * stride + c);
-      sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+    for (int e = 0; e < N; e += 4) {
+      int4 v[S];
+#pragma unroll
+      for (int s = 0; s < S; ++s) v[s] = *reinterpret_cast<const int4*>(p + s * from + c + e);
+      sum[e] = sum[e + 1] = sum[e + 2] = sum[e + 3] = 0;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        sum[e] += v[s].x; sum[e + 1] += v[s].y; sum[e + 2] += v[s].z; sum[e + 3] += v[s].w;
+      }
     }
     const int at = slice * cols + c;
-    out.put(t0 + at, sum.x, sx[at]);
-    out.put(t0 + at + 1, sum.y, sx[at + 1]);
-    out.put(t0 + at + 2, sum.z, sx[at + 2]);
-    out.put(t0 + at + 3, sum.w, sx[at + 3]);
-  }
+    out.put(t0 + at, sum, sx + at);
+  };
+  int c = 0;
+  for (; c + 16 <= cols; c += 16) group(std::integral_constant<int, 16>(), c);
+  for (; c < cols; c += 4) group(std::integral_constant<int, 4>(), c);
 }
 
 // ------------------------------------------------ single CTAs: small batches
@@ -264,7 +336,7 @@ struct TileI8Tail {
   uint64_t full[kI8MaxStages];
   uint64_t empty[kI8MaxStages];
   uint64_t acc;
-  float sx[kI8MaxN];
+  alignas(16) float sx[kI8MaxN];
   uint32_t tmem_slot;
   int abort_flag;
 };
@@ -373,13 +445,8 @@ __global__ void __launch_bounds__(kTileI8Threads)
   const ChannelOut<O> out(P.a, row0 + static_cast<int>(threadIdx.x), *abort_flag == 0);
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
   if constexpr (S == 1) {
-    for (int c0 = 0; c0 < P.n; c0 += 16) {
-      int v[16];
-      tmem_load_16cols(lane_base + c0, v);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) out.put(t0 + c0 + c, v[c], tail.sx[c0 + c]);
-      __syncwarp();
-    }
+    for_columns(lane_base, P.n,
+                [&](int c, const int(&v)[16]) { out.put(t0 + c, v, tail.sx + c); });
   } else {
     // Behind the ring, or over it once every CTA's copies have landed and its
     // MMAs have completed.
@@ -435,7 +502,7 @@ struct PairI8Tail {
   uint64_t empty[kI8MaxStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
-  float sx[kPairI8EpiWarps][kI8MaxN];  // a tile's token scales, per epilogue warp
+  alignas(16) float sx[kPairI8EpiWarps][kI8MaxN];  // a tile's token scales, per epilogue warp
   uint32_t tmem_slot;
   int abort_flag;
 };
@@ -609,19 +676,15 @@ __global__ void __launch_bounds__(kPairI8Threads)
       if constexpr (S == 1) {
         const ChannelOut<O> out(P.a, row, *abort_flag == 0);
         const uint32_t acc = lane_base + static_cast<uint32_t>(b * kI8MaxN);
-        for (int c0 = 0; c0 < P.n; c0 += 16) {
-          int v[16];
-          tmem_load_16cols(acc + c0, v);
-          if (c0 + 16 >= P.n) {  // the accumulator is in registers: hand it back
+        for_columns(acc, P.n, [&](int c, const int(&v)[16]) {
+          if (c + 16 == P.n) {  // the last columns are in registers: hand it back
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
               mbar_arrive_cluster_relaxed(empty0 + b * static_cast<uint32_t>(sizeof(uint64_t)));
           }
-#pragma unroll
-          for (int c = 0; c < 16; ++c) out.put(t0 + c0 + c, v[c], sx[c0 + c]);
-          __syncwarp();
-        }
+          out.put(t0 + c, v, sx + c);
+        });
       }
     }
   }
