@@ -39,7 +39,7 @@ EXPORTED = (
     "dora_compose_fwd_grouped", "dora_compose_bwd_grouped_workspace_size",
     "dora_compose_bwd_grouped", "dora_merge_weight_workspace_size", "dora_merge_weight",
     "dora_factored_norm_sq", "dora_norm_finalize", "dora_compose_fwd_delta",
-    "dora_norm_plan_check", "dora_quantize_rows", "dora_rmsnorm_quant",
+    "dora_norm_plan_check", "dora_quantize_rows", "dora_dequantize_rows", "dora_rmsnorm_quant",
     "dora_linear_i8_workspace_size", "dora_linear_i8",
 )
 
@@ -162,6 +162,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.dora_norm_finalize.restype = c_i
         lib.dora_quantize_rows.argtypes = [c_vp, c_i, c_i64, c_i64, c_vp, c_vp, c_vp]
         lib.dora_quantize_rows.restype = c_i
+        lib.dora_dequantize_rows.argtypes = [c_vp, c_vp, c_i, c_i64, c_i64, c_vp, c_vp]
+        lib.dora_dequantize_rows.restype = c_i
         lib.dora_rmsnorm_quant.argtypes = [c_vp, c_vp, c_vp, c_f, c_i, c_i64, c_i64, c_vp, c_vp,
                                            c_vp, c_vp]
         lib.dora_rmsnorm_quant.restype = c_i
@@ -600,59 +602,106 @@ def dora_norm_finalize(sq: torch.Tensor, m: Optional[torch.Tensor] = None, eps: 
 
 
 # ------------------------------------------------- 8-bit serving of a merged weight
+#
+# These calls run once per layer and decoding step, so their marshalling is
+# kept short: one check per operand that the caller passed, none for what is
+# allocated here, and the current stream's handle without a Stream object.
 
-def _here(t: torch.Tensor, name: str) -> torch.device:
-    """The device of a call's first operand, which must be the current one (the
-    library launches there); the other operands are checked against it."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(t: torch.Tensor, name: str) -> int:
+    """Index of the device of a call's first operand, which must be the current
+    one (the library launches there); the others are checked against it."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    dev = t.device
-    if dev.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor (got {dev})")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {dev} but the current device is "
+    index = t.get_device()
+    if index < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device} but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    return dev
+    return index
 
 
-def _on(dev: torch.device, t: Optional[torch.Tensor], name: str, dtype, shape) -> int:
-    """_dev for an operand that must be on `dev`."""
-    if t is not None and isinstance(t, torch.Tensor) and t.device != dev:
-        raise ValueError(f"{name} must be on {dev} (got {t.device})")
-    return _dev(t, name, dtype, shape)
+def _arg(t: torch.Tensor, name: str, dtype, shape, index: int) -> int:
+    """Data pointer of an operand: dtype, shape, contiguity and device checked."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
+            and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    if isinstance(t, torch.Tensor) and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
+    _dev(t, name, dtype, shape)
+    raise TypeError(f"{name} must be a torch.Tensor")
 
 
-def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+def _current(stream, index: int) -> int:
+    """Handle of the stream a call runs on."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(index)
+    return _stream(stream)
+
+
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     """An output or workspace, allocated for the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) \
-            else torch.cuda.default_stream(dev)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) \
+            else torch.cuda.default_stream(like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _matrix(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions (got shape {tuple(t.shape)})")
     return t.shape
+
+
+def _out(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dtype, index: int,
+         stream):
+    """An output the caller passed, or a new one: (tensor, its pointer)."""
+    if t is None:
+        t = _new(like, shape, dtype, stream)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, index)
 
 
 def dora_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
                        scale: Optional[torch.Tensor] = None, stream=None):
     """int8 codes and fp32 scales of the rows of x ([rows, cols], fp32 or bf16):
     x is approximately q * scale[:, None].  Returns (q, scale)."""
-    lib = load_library()
-    dev = _here(x, "x")
+    lib = _lib or load_library()
+    index = _here(x, "x")
     dt = _dtype_code(x)
-    rows, cols = _matrix(x, "x")
-    q = _new((rows, cols), torch.int8, dev, stream) if q is None else q
-    scale = _new((rows,), torch.float32, dev, stream) if scale is None else scale
-    _check(lib.dora_quantize_rows(
-        _dev(x, "x"), dt, rows, cols, _on(dev, q, "q", torch.int8, (rows, cols)),
-        _on(dev, scale, "scale", torch.float32, (rows,)), _stream(stream)), "dora_quantize_rows")
+    shape = rows, cols = _matrix(x, "x")
+    q, pq = _out(q, "q", x, shape, torch.int8, index, stream)
+    scale, ps = _out(scale, "scale", x, (rows,), torch.float32, index, stream)
+    _check(lib.dora_quantize_rows(_arg(x, "x", x.dtype, shape, index), dt, rows, cols, pq, ps,
+                                  _current(stream, index)), "dora_quantize_rows")
     return q, scale
+
+
+def dora_dequantize_rows(q: torch.Tensor, scale: torch.Tensor,
+                         dtype: torch.dtype = torch.bfloat16, x: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """The values q * scale[:, None] that int8 codes stand for, in `dtype` (bf16
+    or fp32; x's own where x is given)."""
+    lib = _lib or load_library()
+    index = _here(q, "q")
+    shape = rows, cols = _matrix(q, "q")
+    dtype = x.dtype if isinstance(x, torch.Tensor) else dtype
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}: the library takes float32 or bfloat16")
+    pq = _arg(q, "q", torch.int8, shape, index)
+    ps = _arg(scale, "scale", torch.float32, (rows,), index)
+    x, px = _out(x, "x", q, shape, dtype, index, stream)
+    _check(lib.dora_dequantize_rows(pq, ps, _DT[dtype], rows, cols, px, _current(stream, index)),
+           "dora_dequantize_rows")
+    return x
 
 
 def dora_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float,
@@ -662,21 +711,24 @@ def dora_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float,
     """h = x + residual; int8 codes and fp32 scales per token of the RMS norm of
     h times weight.  Returns (q, scale, h), h None without a residual.  h_out
     may be x or residual itself."""
-    lib = load_library()
-    dev = _here(x, "x")
+    lib = _lib or load_library()
+    index = _here(x, "x")
     dt = _dtype_code(x)
-    T, d = _matrix(x, "x")
-    if residual is None and h_out is not None:
+    shape = T, d = _matrix(x, "x")
+    dtype = x.dtype
+    px = _arg(x, "x", dtype, shape, index)
+    pw = _arg(weight, "weight", dtype, (d,), index)
+    if residual is not None:
+        pr = _arg(residual, "residual", dtype, shape, index)
+        h_out, ph = _out(h_out, "h_out", x, shape, dtype, index, stream)
+    elif h_out is None:
+        pr = ph = None
+    else:
         raise ValueError("h_out is the sum with a residual: pass residual too")
-    if residual is not None and h_out is None:
-        h_out = _new((T, d), x.dtype, dev, stream)
-    q = _new((T, d), torch.int8, dev, stream) if q is None else q
-    scale = _new((T,), torch.float32, dev, stream) if scale is None else scale
-    _check(lib.dora_rmsnorm_quant(
-        _dev(x, "x"), _on(dev, residual, "residual", x.dtype, (T, d)),
-        _on(dev, weight, "weight", x.dtype, (d,)), float(eps), dt, T, d,
-        _on(dev, h_out, "h_out", x.dtype, (T, d)), _on(dev, q, "q", torch.int8, (T, d)),
-        _on(dev, scale, "scale", torch.float32, (T,)), _stream(stream)), "dora_rmsnorm_quant")
+    q, pq = _out(q, "q", x, shape, torch.int8, index, stream)
+    scale, ps = _out(scale, "scale", x, (T,), torch.float32, index, stream)
+    _check(lib.dora_rmsnorm_quant(px, pr, pw, float(eps), dt, T, d, ph, pq, ps,
+                                  _current(stream, index)), "dora_rmsnorm_quant")
     return q, scale, h_out
 
 
@@ -691,24 +743,28 @@ def dora_linear_i8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor,
     """y[t, j] = (xq[t] . wq[j]) x_scale[t] w_scale[j] (+ bias[j]) in `dtype`
     (bf16 or fp32; y's own where y is given).  xq [T, d_in], wq [d_out, d_in]
     int8; scales and bias fp32."""
-    lib = load_library()
-    dev = _here(xq, "xq")
+    lib = _lib or load_library()
+    index = _here(xq, "xq")
     T, d_in = _matrix(xq, "xq")
     d_out = _matrix(wq, "wq")[0]
-    if y is None:
-        if dtype not in _DT:
-            raise TypeError(f"unsupported dtype {dtype}: the library takes float32 or bfloat16")
-        y = _new((T, d_out), dtype, dev, stream)
-    dt = _dtype_code(y)
-    need = lib.dora_linear_i8_workspace_size(T, d_out, d_in)
-    if ws is None and need > 0:
-        ws = _new((need,), torch.uint8, dev, stream)
-    _check(lib.dora_linear_i8(
-        _dev(xq, "xq", torch.int8), _on(dev, x_scale, "x_scale", torch.float32, (T,)),
-        _on(dev, wq, "wq", torch.int8, (d_out, d_in)),
-        _on(dev, w_scale, "w_scale", torch.float32, (d_out,)),
-        _on(dev, bias, "bias", torch.float32, (d_out,)), dt, T, d_out, d_in,
-        _on(dev, y, "y", y.dtype, (T, d_out)),
-        0 if ws is None else _on(dev, ws, "ws", None, None),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "dora_linear_i8")
+    px = _arg(xq, "xq", torch.int8, (T, d_in), index)
+    psx = _arg(x_scale, "x_scale", torch.float32, (T,), index)
+    pw = _arg(wq, "wq", torch.int8, (d_out, d_in), index)
+    psw = _arg(w_scale, "w_scale", torch.float32, (d_out,), index)
+    pb = None if bias is None else _arg(bias, "bias", torch.float32, (d_out,), index)
+    dtype = y.dtype if isinstance(y, torch.Tensor) else dtype
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}: the library takes float32 or bfloat16")
+    y, py = _out(y, "y", xq, (T, d_out), dtype, index, stream)
+    pws, nws = None, 0
+    if ws is None and d_in % 16:  # rows of whole 16-byte steps need no workspace
+        nws = lib.dora_linear_i8_workspace_size(T, d_out, d_in)
+        if nws:
+            ws = _new(xq, (nws,), torch.uint8, stream)
+            pws = ws.data_ptr()
+    elif ws is not None:
+        pws = _arg(ws, "ws", ws.dtype, ws.shape, index)
+        nws = ws.numel() * ws.element_size()
+    _check(lib.dora_linear_i8(px, psx, pw, psw, pb, _DT[dtype], T, d_out, d_in, py, pws, nws,
+                              _current(stream, index)), "dora_linear_i8")
     return y

@@ -2065,6 +2065,16 @@ dora_status_t run_rows(const RowArgs& P, dora_dtype_t dt, int mode, dora_stream_
   return launch_status();
 }
 
+template <typename E, int VEC>
+void launch_dequant(const int8_t* q, const float* scale, int64_t rows, int cols, void* x,
+                    cudaStream_t cs) {
+  const StreamGrid g = stream_grid(rows, static_cast<int>(ceil_div_ll(cols, VEC)),
+                                   kDequantRowUnroll, 4 * kStreamSlots);
+  launch_stream(dequant_rows_kernel<E, VEC>, dim3(g.gx, std::min(g.gy, 65535)),
+                dim3(kStreamThreads), 0, cs, q, scale, static_cast<long long>(rows), cols,
+                static_cast<E*>(x), g.bx);
+}
+
 // ---- linear layer
 
 template <typename O, int TT>
@@ -2290,6 +2300,38 @@ dora_status_t dora_quantize_rows(const void* x, dora_dtype_t dt, int64_t rows, i
   if (rows > kMaxQuantRows || cols > kMaxQuantCols) return DORA_ERR_UNSUPPORTED;
   const RowArgs P{x, nullptr, nullptr, nullptr, q, scale, rows, static_cast<int>(cols), 0.f};
   return run_rows(P, dt, kRowQuant, stream);
+}
+
+dora_status_t dora_dequantize_rows(const int8_t* q, const float* scale, dora_dtype_t dt,
+                                   int64_t rows, int64_t cols, void* x, dora_stream_t stream) {
+  if (dt != DORA_F32 && dt != DORA_BF16) return DORA_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 1) return DORA_ERR_INVALID_ARG;
+  if (rows > 0 && (x == nullptr || q == nullptr || scale == nullptr)) return DORA_ERR_INVALID_ARG;
+  if (rows > kMaxQuantRows || cols > kMaxQuantCols) return DORA_ERR_UNSUPPORTED;
+  const size_t es = dt == DORA_BF16 ? 2 : 4, n = static_cast<size_t>(rows) * cols;
+  if (!aligned_to(x, es) || !aligned_to(scale, 4)) return DORA_ERR_INVALID_ARG;
+  if (overlaps(x, n * es, q, n) || overlaps(x, n * es, scale, static_cast<size_t>(rows) * 4))
+    return DORA_ERR_INVALID_ARG;
+  const DeviceInfo* di = device_info();
+  if (di == nullptr) return DORA_ERR_CUDA;
+  if (!di->supported) return DORA_ERR_UNSUPPORTED;
+  if (rows == 0) return DORA_OK;
+  const int v = dt == DORA_BF16 ? 8 : 4, c = static_cast<int>(cols);
+  const bool vec = cols % v == 0 && aligned16(x) && aligned_to(q, v);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  TimedLaunch tl(cs);
+  if (dt == DORA_BF16) {
+    if (vec)
+      launch_dequant<__nv_bfloat16, 8>(q, scale, rows, c, x, cs);
+    else
+      launch_dequant<__nv_bfloat16, 1>(q, scale, rows, c, x, cs);
+  } else {
+    if (vec)
+      launch_dequant<float, 4>(q, scale, rows, c, x, cs);
+    else
+      launch_dequant<float, 1>(q, scale, rows, c, x, cs);
+  }
+  return launch_status();
 }
 
 dora_status_t dora_rmsnorm_quant(const void* x, const void* residual, const void* weight,

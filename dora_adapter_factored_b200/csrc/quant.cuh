@@ -20,6 +20,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "compose.cuh"
 #include "sm100.cuh"
 
 namespace dora {
@@ -327,6 +328,62 @@ __global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowAr
         for (int e = 0; e < VEC; ++e) u[e] = 0.f;
       }
       store_codes<VEC>(P.q + at + static_cast<size_t>(c) * VEC, u, inv);
+    }
+  }
+}
+
+// The values that codes stand for: x = q scale, one rounding.  A stream in the
+// shape of the compose kernels: a thread keeps its columns and walks rows,
+// several rows' codes in flight.
+constexpr int kDequantRowUnroll = 8;
+
+template <typename E, int VEC>
+struct CodeVec;
+template <typename E>
+struct CodeVec<E, 8> { using raw = uint2; };
+template <typename E>
+struct CodeVec<E, 4> { using raw = uint32_t; };
+template <typename E>
+struct CodeVec<E, 1> { using raw = uint8_t; };
+
+__device__ __forceinline__ uint32_t code_word(const uint2& r, int i) { return i ? r.y : r.x; }
+__device__ __forceinline__ uint32_t code_word(uint32_t r, int) { return r; }
+__device__ __forceinline__ uint32_t code_word(uint8_t r, int) { return r; }
+
+template <typename E, int VEC>
+__global__ void __launch_bounds__(kStreamThreads)
+    dequant_rows_kernel(const int8_t* q, const float* scale, long long rows, int cols, E* x,
+                        int bx) {
+  using raw = typename CodeVec<E, VEC>::raw;
+  const int by = kStreamThreads / bx;
+  const int c = (static_cast<int>(blockIdx.x) * bx + static_cast<int>(threadIdx.x) % bx) * VEC;
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  if (c >= cols) return;
+  const long long step = static_cast<long long>(gridDim.y) * by;
+  for (long long r0 = static_cast<long long>(blockIdx.y) * by + threadIdx.x / bx; r0 < rows;
+       r0 += step * kDequantRowUnroll) {
+    raw v[kDequantRowUnroll];
+    float s[kDequantRowUnroll];
+#pragma unroll
+    for (int u = 0; u < kDequantRowUnroll; ++u) {
+      const long long r = r0 + u * step;
+      if (r < rows) {
+        v[u] = *reinterpret_cast<const raw*>(q + static_cast<size_t>(r) * cols + c);
+        s[u] = scale[r];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kDequantRowUnroll; ++u) {
+      const long long r = r0 + u * step;
+      if (r >= rows || !DORA_BOUNDS_OK(c + VEC <= cols)) continue;
+      float o[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        o[e] = static_cast<float>(static_cast<int8_t>(code_word(v[u], e / 4) >> (8 * (e % 4)))) *
+               s[u];
+      *reinterpret_cast<typename RowVec<E, VEC>::raw*>(x + static_cast<size_t>(r) * cols + c) =
+          RowVec<E, VEC>::pack(o);
     }
   }
 }

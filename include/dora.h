@@ -322,6 +322,7 @@ dora_status_t dora_merge_weight(const void *W0, const void *A, const void *B, co
  *   per layer: dora_rmsnorm_quant   hidden states     -> xq, x_scale (and h)
  *              (or dora_quantize_rows where no norm precedes the layer)
  *              dora_linear_i8       xq, wq            -> y = x W'^T
+ *   and back:  dora_dequantize_rows q, scale          -> values
  *
  * A row v of values is held as  scale = max_j |v_j| / 127  and
  * q_j = round(v_j / scale), half to even, in [-127, 127]; v_j is then
@@ -337,11 +338,19 @@ dora_status_t dora_merge_weight(const void *W0, const void *A, const void *B, co
 
 /* Rows of x [rows, cols] (dtype `dt`) to codes q [rows, cols] and scale
  * [rows] fp32.  Outputs must not overlap x or each other.  rows == 0 launches
- * nothing.  rows, cols <= 2^30.  One launch, one pass over x for rows up to
- * 16384 bf16 or 8192 fp32 elements (half that where rows are not 16-byte
- * aligned), else two. */
+ * nothing.  rows, cols <= 2^30.  One launch; x is read once where a row fits
+ * the registers of a block (16384 bf16 or 8192 fp32 elements; 8192 where rows
+ * are not 16-byte aligned), else twice. */
 dora_status_t dora_quantize_rows(const void *x, dora_dtype_t dt, int64_t rows, int64_t cols,
                                  int8_t *q, float *scale, dora_stream_t stream);
+
+/* The values that codes stand for: x[i, j] = q[i, j] scale[i], rounded once to
+ * `dt`; NaN in a row whose scale is NaN.  For a weight held as codes that a
+ * call of this library reads in bf16 or fp32 (W0 of the norm and the merge), or
+ * for what reads activations unquantised.  x [rows, cols] must not overlap q
+ * or scale.  rows == 0 launches nothing.  rows, cols <= 2^30.  One launch. */
+dora_status_t dora_dequantize_rows(const int8_t *q, const float *scale, dora_dtype_t dt,
+                                   int64_t rows, int64_t cols, void *x, dora_stream_t stream);
 
 /* RMS norm with the residual's addition and quantised output, per token t:
  *   h = x + residual, rounded to `dt` and written to h_out (or h = x where

@@ -44,6 +44,10 @@ def _quant(lib, x=X, dt=BF16, rows=4, cols=64, q=Q, scale=S):
     return lib.dora_quantize_rows(x, dt, rows, cols, q, scale, None)
 
 
+def _deq(lib, q=Q, scale=S, dt=BF16, rows=4, cols=64, x=X):
+    return lib.dora_dequantize_rows(q, scale, dt, rows, cols, x, None)
+
+
 def _norm(lib, x=X, r=R, w=W, eps=1e-6, dt=BF16, T=4, d=64, h=H, q=Q, scale=S):
     return lib.dora_rmsnorm_quant(x, r, w, eps, dt, T, d, h, q, scale, None)
 
@@ -64,6 +68,13 @@ BAD_QUANT = [
     (dict(q=vp(0x10001ff)), INVALID),             # ... over its last byte
     (dict(scale=vp(0x1000004)), INVALID),         # scale over x
     (dict(scale=vp(0x5000004)), INVALID),         # scale over the codes
+]
+BAD_DEQ = [
+    (dict(x=None), INVALID), (dict(q=None), INVALID), (dict(scale=None), INVALID),
+    (dict(dt=2), INVALID), (dict(rows=-1), INVALID), (dict(cols=0), INVALID),
+    (dict(cols=(1 << 30) + 1), UNSUPPORTED), (dict(rows=(1 << 30) + 1), UNSUPPORTED),
+    (dict(x=vp(0x1000001)), INVALID), (dict(x=vp(0x1000002), dt=F32), INVALID),
+    (dict(scale=vp(0x6000002)), INVALID), (dict(x=Q), INVALID), (dict(x=S), INVALID),
 ]
 BAD_NORM = [
     (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(q=None), INVALID),
@@ -89,8 +100,9 @@ BAD_LINEAR = [
 ]
 
 
-@pytest.mark.parametrize("call,bad", [(_quant, BAD_QUANT), (_norm, BAD_NORM),
-                                      (_linear, BAD_LINEAR)], ids=["quant", "norm", "linear"])
+@pytest.mark.parametrize("call,bad", [(_quant, BAD_QUANT), (_deq, BAD_DEQ), (_norm, BAD_NORM),
+                                      (_linear, BAD_LINEAR)],
+                         ids=["quantize", "dequantize", "norm", "linear"])
 def test_host_validation(built_library, call, bad):
     lib = dora.load_library(built_library)
     before = dora.dora_launch_count()
@@ -122,6 +134,7 @@ def test_valid_arguments_reach_the_device_check(built_library):
         pytest.skip("a GPU is present")
     lib = dora.load_library(built_library)
     for call, kws in ((_quant, [{}, dict(rows=0, x=None, q=None, scale=None)]),
+                      (_deq, [{}, dict(rows=0, x=None, q=None, scale=None)]),
                       (_norm, [{}, dict(h=X), dict(h=R), dict(r=None, h=None),
                                dict(T=0, x=None, r=None, h=None, q=None, scale=None)]),
                       (_linear, [{}, dict(bias=vp(0x7000000)), dict(d_in=131071),
@@ -141,5 +154,7 @@ def test_binding_refusals(built_library):
         dora.dora_rmsnorm_quant(x, x[0], 1e-6)
     with pytest.raises(ValueError, match="CUDA tensor"):
         dora.dora_linear_i8(x.char(), torch.ones(4), x.char(), torch.ones(4))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        dora.dora_dequantize_rows(x.char(), torch.ones(4))
     with pytest.raises(TypeError, match="torch.Tensor"):
         dora.dora_quantize_rows([[1.0]])

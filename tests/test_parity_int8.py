@@ -188,6 +188,40 @@ def test_halves_go_to_even():
     assert q[0, :8].tolist() == [127, 0, 2, 2, 0, -2, 4, 126]
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(1, 1), (3, 7), (2, 64), (5, 1000), (9, 1001), (700, 264),
+                                 (2500, 33), (41, 40000), (1, 8192)])
+def test_dequantize_rows(T, d, dt):
+    """One fp32 product, and for bf16 its rounding: bit for bit."""
+    q, scale = _codes(T, d, T + d), _scales(T, d)
+    if T > 2:
+        scale[1], scale[2] = float("nan"), 0.0
+    want = (q.cpu().float() * scale.cpu()[:, None]).to(DTYPES[dt])
+    x = dora.dora_dequantize_rows(q, scale, DTYPES[dt])
+    assert torch.equal(torch.isnan(x.cpu()), torch.isnan(want))
+    assert torch.equal(x.cpu().nan_to_num(), want.nan_to_num())
+    # operands and result off their boundaries
+    qb = torch.empty(T * d + 3, dtype=torch.int8, device="cuda")[3:].view(T, d).copy_(q)
+    xb, xw, xg = _guarded(T * d + 1, DTYPES[dt])
+    out = dora.dora_dequantize_rows(qb, scale, x=xb[1:].view(T, d))
+    _intact((xw, xg))
+    assert torch.equal(out.nan_to_num(), x.nan_to_num())
+
+
+def test_weight_held_as_codes_through_norm_and_merge():
+    """A quantised base weight, dequantised for the calls that read bf16."""
+    W0 = _rand(96, 256, "bf16", 1, 0.02)
+    A, B = _rand(16, 256, "bf16", 2, 0.03), _rand(96, 16, "bf16", 3, 0.02)
+    q, scale = dora.dora_quantize_rows(W0)
+    W = dora.dora_dequantize_rows(q, scale)
+    n, _ = dora.dora_factored_norm(W, A, B, 2.0)
+    ref = oracle.dense_row_norm(_np(W), _np(A), _np(B), 2.0)
+    assert np.max(np.abs(_np(n) - ref) / ref) < 1e-3
+    half = 0.5 + 127 * 2 * U + 1e-4  # half a step of each row, and bf16's rounding
+    assert (np.abs(_np(W) - _np(W0)) <= half * _np(scale)[:, None] + 2.0 ** -8 * np.abs(_np(W0))
+            + 2.0 ** -8 * _np(scale)[:, None]).all()
+
+
 @pytest.mark.parametrize("over", ["x", "residual"])
 @pytest.mark.parametrize("d", [1024, 999, 40000])
 def test_h_in_place(over, d):
@@ -310,6 +344,7 @@ def test_no_rows():
     assert q.shape == (0, 64) and s.shape == (0,)
     q, s, h = dora.dora_rmsnorm_quant(x, w, EPS, residual=x.clone())
     assert h.shape == (0, 64)
+    assert dora.dora_dequantize_rows(q, s).shape == (0, 64)
     y = dora.dora_linear_i8(q, s, _codes(8, 64, 1), _scales(8, 1))
     assert y.shape == (0, 8)
     assert dora.dora_launch_count() == before
@@ -353,7 +388,7 @@ def _layer(x, r, w, wq, sw, bias, stream=None):
     q, s, h = dora.dora_rmsnorm_quant(x, w, EPS, residual=r, stream=stream)
     y = dora.dora_linear_i8(q, s, wq, sw, bias=bias, stream=stream)
     q2, s2 = dora.dora_quantize_rows(y, stream=stream)
-    return h, q, s, y, q2, s2
+    return h, q, s, y, q2, s2, dora.dora_dequantize_rows(q2, s2, stream=stream)
 
 
 @pytest.mark.parametrize("T", [1, 24, 150, 600])
@@ -371,7 +406,7 @@ def test_streams_and_graphs(T):
         got = _layer(x, r, w, wq, sw, bias, stream=a)
         got2 = _layer(r, x, w, wq, sw, bias, stream=b.cuda_stream)
     torch.cuda.synchronize()
-    for k in range(6):
+    for k in range(7):
         assert torch.equal(ref[k], got[k]) and torch.equal(ref2[k], got2[k])
     xs, rs = x.clone(), r.clone()
     graph = torch.cuda.CUDAGraph()
@@ -415,6 +450,12 @@ def test_refusals():
     with pytest.raises(dora.DoraError):
         dora.dora_rmsnorm_quant(x, w, EPS, residual=x.clone(), h_out=w.new_zeros(4, 64),
                                 q=q, scale=x.view(-1).view(torch.float32)[:4])
+    with pytest.raises(TypeError, match="dtype"):
+        dora.dora_dequantize_rows(q, s, torch.float16)
+    with pytest.raises(ValueError, match="contiguous"):
+        dora.dora_dequantize_rows(q.t(), torch.ones(64, device="cuda"))
+    with pytest.raises(ValueError, match="x must have shape"):
+        dora.dora_dequantize_rows(q, s, x=x[:2])
     with pytest.raises(TypeError, match="xq must be"):
         dora.dora_linear_i8(x, s, q, s)
     with pytest.raises(ValueError, match="wq must have shape"):
