@@ -164,6 +164,12 @@ constexpr int kI8MaxN = 256;
 constexpr int kI8MaxStages = 12;
 constexpr uint32_t kI8WBytes = kI8M * kI8K;  // 16 KiB of weight per stage and CTA
 
+// A wait of a whole (converged) warp: the same answer in every lane.
+__device__ __forceinline__ bool i8_wait(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+                                        const volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_fast(bar, parity, timeout_ns, abort));
+}
+
 __device__ __forceinline__ void linear_give_up(volatile int* abort_flag) {
   *abort_flag = 1;
   record_error(DORA_ERR_TIMEOUT);
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kTileI8Threads)
                                              ~static_cast<uintptr_t>(1023));
   __shared__ TileI8Tail tail;
   volatile int* abort_flag = &tail.abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int slice = static_cast<int>(blockIdx.x) % S;  // = rank in the cluster
   const int row0 = static_cast<int>(blockIdx.x) / S * kI8M;
   const int t0 = static_cast<int>(blockIdx.y) * P.n;
@@ -386,60 +392,64 @@ __global__ void __launch_bounds__(kTileI8Threads)
   grid_dependency_trigger();  // not before TMEM is held: the next grid may want it too
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      for (int k = kb0; k < kb1; ++k) {
-        if (!mbar_wait(&tail.empty[stage], phase ^ 1u, timeout_ns, abort_flag)) {
-          linear_give_up(abort_flag);
-          break;
-        }
+    const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    for (int k = kb0; k < kb1; ++k) {
+      if (!i8_wait(&tail.empty[stage], phase ^ 1u, timeout_ns, abort_flag)) {
+        linear_give_up(abort_flag);
+        break;
+      }
+      if (elect_one()) {
         uint8_t* st = ring + stage * stage_bytes;
         mbar_arrive_expect_tx(&tail.full[stage], stage_bytes);
         tma_load_2d(st, &P.tm_w, &tail.full[stage], k * kI8K, row0, pol_w);
         tma_load_2d(st + kI8WBytes, &P.tm_x, &tail.full[stage], k * kI8K, t0, pol_x);
-        ++issued;
-        if (++stage == P.stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      // Every copy lands before the CTA can exit, also after a give-up.
-      for (int j = max(0, issued - P.stages); j < issued; ++j)
-        mbar_wait(&tail.full[j % P.stages], static_cast<uint32_t>((j / P.stages) & 1),
-                  kDrainTimeoutNs, nullptr);
+      __syncwarp();
+      ++issued;
+      if (++stage == P.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
+    // Every copy lands before the CTA can exit, also after a give-up.
+    for (int j = max(0, issued - P.stages); j < issued; ++j)
+      mbar_wait(&tail.full[j % P.stages], static_cast<uint32_t>((j / P.stages) & 1),
+                kDrainTimeoutNs, nullptr);
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int k = kb0; k < kb1; ++k) {
-        if (!mbar_wait(&tail.full[stage], phase, timeout_ns, abort_flag)) {
-          linear_give_up(abort_flag);
-          break;
-        }
-        tc_fence_after_sync();
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int k = kb0; k < kb1; ++k) {
+      if (!i8_wait(&tail.full[stage], phase, timeout_ns, abort_flag)) {
+        linear_give_up(abort_flag);
+        break;
+      }
+      tc_fence_after_sync();
+      if (elect_one()) {
         const uint32_t w = smem_addr(ring + stage * stage_bytes), x = w + kI8WBytes;
 #pragma unroll
         for (int kk = 0; kk < kI8K / 32; ++kk)
           umma_i8(tmem, sw128_kmajor_desc(w + kk * 32), sw128_kmajor_desc(x + kk * 32), P.idesc,
                   (k > kb0 || kk > 0) ? 1u : 0u);
         umma_commit(&tail.empty[stage]);
-        if (++stage == P.stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      umma_commit(&tail.acc);  // also after a give-up: completes once the issued MMAs have
-      mbar_wait(&tail.acc, 0, kDrainTimeoutNs, nullptr);
+      __syncwarp();
+      if (++stage == P.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
+    // Also after a give-up: completes once the issued MMAs have.
+    if (elect_one()) umma_commit(&tail.acc);
+    __syncwarp();
+    mbar_wait(&tail.acc, 0, kDrainTimeoutNs, nullptr);
   } else {
     for (int c = static_cast<int>(threadIdx.x) - 64; c < P.n; c += 64)
       tail.sx[c] = t0 + c < P.a.T ? P.a.x_scale[t0 + c] : 0.f;
   }
   __syncwarp();
-  if (!mbar_wait(&tail.acc, 0, timeout_ns, abort_flag)) linear_give_up(abort_flag);
+  if (!mbar_wait_fast(&tail.acc, 0, timeout_ns, abort_flag)) linear_give_up(abort_flag);
   __syncthreads();  // every wait is over, sx is written
   tc_fence_after_sync();
   const ChannelOut<O> out(P.a, row0 + static_cast<int>(threadIdx.x), *abort_flag == 0);
@@ -528,7 +538,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
                                              ~static_cast<uintptr_t>(1023));
   __shared__ PairI8Tail tail;
   volatile int* abort_flag = &tail.abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank(), half = rank & 1u, lead = rank & ~1u;
   const int slice = static_cast<int>(rank >> 1);
   const uint32_t peer_abort = mapa_shared(smem_addr(&tail.abort_flag), rank ^ 1u);
@@ -573,82 +583,88 @@ __global__ void __launch_bounds__(kPairI8Threads)
 
   if (warp == kPairI8EpiWarps) {
     // ---------------------------------------------------------- copy producer
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_last();
-      const uint32_t full0 = mapa_shared(smem_addr(&tail.full[0]), lead);
-      int stage = 0;
-      uint32_t phase = 0;
-      long long issued = 0;
-      bool ok = true;
-      for (int i = first; ok && i < tiles; i += step) {
-        int tm, tn;
-        pair_tile(P, i, tm, tn);
-        const int row = tm * 2 * kI8M + static_cast<int>(half) * kI8M;
-        const int tok = tn * P.n + static_cast<int>(half) * (P.n / 2);
-        for (int k = kb0; k < kb1; ++k) {
-          if (!mbar_wait(&tail.empty[stage], phase ^ 1u, timeout_ns, abort_flag)) {
-            give_up();
-            ok = false;
-            break;
-          }
+    const uint64_t pol = policy_evict_last();
+    const uint32_t full0 = mapa_shared(smem_addr(&tail.full[0]), lead);
+    int stage = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool ok = true;
+    for (int i = first; ok && i < tiles; i += step) {
+      int tm, tn;
+      pair_tile(P, i, tm, tn);
+      const int row = tm * 2 * kI8M + static_cast<int>(half) * kI8M;
+      const int tok = tn * P.n + static_cast<int>(half) * (P.n / 2);
+      for (int k = kb0; k < kb1; ++k) {
+        if (!i8_wait(&tail.empty[stage], phase ^ 1u, timeout_ns, abort_flag)) {
+          give_up();
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           uint8_t* st = ring + stage * stage_bytes;
           const uint32_t bar = full0 + stage * static_cast<uint32_t>(sizeof(uint64_t));
           if (half == 0) mbar_arrive_expect_tx(&tail.full[stage], 2 * stage_bytes);
           tma_load_2d_pair(st, &P.tm_w, bar, k * kI8K, row, pol);
           tma_load_2d_pair(st + kI8WBytes, &P.tm_x, bar, k * kI8K, tok, pol);
-          ++issued;
-          if (++stage == P.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == P.stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // Every copy lands before the CTA can exit: rank 0 sees its full
-      // barriers complete; rank 1's copies complete on those, so it waits for
-      // its stages to be consumed.
-      for (long long j = issued > P.stages ? issued - P.stages : 0; j < issued; ++j) {
-        const uint32_t par = static_cast<uint32_t>((j / P.stages) & 1);
-        mbar_wait(half == 0 ? &tail.full[j % P.stages] : &tail.empty[j % P.stages], par,
-                  kDrainTimeoutNs, nullptr);
-      }
+    }
+    // Every copy lands before the CTA can exit: rank 0 sees its full barriers
+    // complete; rank 1's copies complete on those, so it waits for its stages
+    // to be consumed.
+    for (long long j = issued > P.stages ? issued - P.stages : 0; j < issued; ++j) {
+      const uint32_t par = static_cast<uint32_t>((j / P.stages) & 1);
+      mbar_wait(half == 0 ? &tail.full[j % P.stages] : &tail.empty[j % P.stages], par,
+                kDrainTimeoutNs, nullptr);
     }
   } else if (warp == kPairI8EpiWarps + 1) {
     // ------------------------------------------------------------- MMA issuer
-    if (lane == 0 && half == 0) {
+    if (half == 0) {
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int i = first; ok && i < tiles; i += step, ++it) {
         const int b = it & 1;
-        if (!mbar_wait(&tail.acc_empty[b], static_cast<uint32_t>(((it >> 1) & 1) ^ 1), timeout_ns,
-                       abort_flag)) {
+        if (!i8_wait(&tail.acc_empty[b], static_cast<uint32_t>(((it >> 1) & 1) ^ 1), timeout_ns,
+                     abort_flag)) {
           give_up();
           break;
         }
         tc_fence_after_sync();
         const uint32_t d = tmem + static_cast<uint32_t>(b * kI8MaxN);
         for (int k = kb0; k < kb1; ++k) {
-          if (!mbar_wait(&tail.full[stage], phase, timeout_ns, abort_flag)) {
+          if (!i8_wait(&tail.full[stage], phase, timeout_ns, abort_flag)) {
             give_up();
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t w = smem_addr(ring + stage * stage_bytes), x = w + kI8WBytes;
+          if (elect_one()) {
+            const uint32_t w = smem_addr(ring + stage * stage_bytes), x = w + kI8WBytes;
 #pragma unroll
-          for (int kk = 0; kk < kI8K / 32; ++kk)
-            umma_i8_pair(d, sw128_kmajor_desc(w + kk * 32), sw128_kmajor_desc(x + kk * 32),
-                         P.idesc, (k > kb0 || kk > 0) ? 1u : 0u);
-          umma_commit_pair(&tail.empty[stage], pair_mask);
+            for (int kk = 0; kk < kI8K / 32; ++kk)
+              umma_i8_pair(d, sw128_kmajor_desc(w + kk * 32), sw128_kmajor_desc(x + kk * 32),
+                           P.idesc, (k > kb0 || kk > 0) ? 1u : 0u);
+            umma_commit_pair(&tail.empty[stage], pair_mask);
+          }
+          __syncwarp();
           if (++stage == P.stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        umma_commit_pair(&tail.acc_full[b], pair_mask);
+        if (elect_one()) umma_commit_pair(&tail.acc_full[b], pair_mask);
+        __syncwarp();
       }
       // Also after a give-up: no MMA is in flight when the CTAs leave.
-      umma_commit_pair(&tail.drain, static_cast<uint16_t>(1u << lead));
+      if (elect_one()) umma_commit_pair(&tail.drain, static_cast<uint16_t>(1u << lead));
+      __syncwarp();
       mbar_wait(&tail.drain, 0, kDrainTimeoutNs, nullptr);
     }
   } else {
@@ -667,7 +683,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
         sx[c] = t0 + c < P.a.T ? P.a.x_scale[t0 + c] : 0.f;
       __syncwarp();
       if (!__all_sync(0xffffffffu,
-                      mbar_wait(&tail.acc_full[b], static_cast<uint32_t>((it >> 1) & 1),
+                      mbar_wait_fast(&tail.acc_full[b], static_cast<uint32_t>((it >> 1) & 1),
                                 timeout_ns, abort_flag))) {
         give_up();
         break;

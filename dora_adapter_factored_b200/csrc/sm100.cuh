@@ -109,6 +109,33 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   }
 }
 
+// As mbar_wait for waits in a pipeline's inner loop: the global timer is left
+// alone until some tries have failed.
+__device__ __forceinline__ bool mbar_wait_fast(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+                                               const volatile int* abort) {
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, timeout_ns, abort);
+}
+
+// True in one lane of the (converged) warp, the same one every time.  Code
+// under it is known to run in a single thread, so that the operands of MMAs
+// and bulk copies stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(one));
+  return one != 0;
+}
+
+// The warp's index as a value the compiler knows to be the same in all lanes.
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
+}
+
 // ---------------------------------------------------------------- PDL
 // Programmatic dependent launch: wait for the preceding grid to complete and
 // its writes to be visible; allow the next grid to launch.
