@@ -175,6 +175,53 @@ __device__ __forceinline__ void linear_give_up(volatile int* abort_flag) {
   record_error(DORA_ERR_TIMEOUT);
 }
 
+// The MMA issuer's k loop, shared by both kernels: a converged warp walks the
+// stages and an elected lane issues a k-block's MMAs and the commit that frees
+// the stage.  The loop has to turn around faster than a k-block's MMAs run
+// (256 cycles at N = 128), so the next stage's barrier is tried before this
+// one's MMAs are issued, and the descriptors are 32-bit sums (the low words;
+// a stage or a K step only moves the start address).  Returns false after a
+// give-up.
+struct I8Stage {
+  int stage;
+  uint32_t phase;
+};
+
+template <typename Mma, typename Commit, typename GiveUp>
+__device__ __forceinline__ bool i8_mma_loop(int kblocks, int stages, uint32_t ring,
+                                            uint32_t stage_bytes, uint64_t* full, I8Stage& at,
+                                            unsigned long long timeout_ns,
+                                            const volatile int* abort_flag, Mma&& mma,
+                                            Commit&& commit, GiveUp&& give_up) {
+  const uint64_t d0 = sw128_kmajor_desc(ring);
+  const uint32_t base = static_cast<uint32_t>(d0);
+  const uint64_t high = d0 & 0xFFFFFFFF00000000ull;
+  bool ready = mbar_try_wait(&full[at.stage], at.phase);
+  for (int k = 0; k < kblocks; ++k) {
+    if (!__all_sync(0xffffffffu, ready) &&
+        !i8_wait(&full[at.stage], at.phase, timeout_ns, abort_flag)) {
+      give_up();
+      return false;
+    }
+    const int stage = at.stage;
+    if (++at.stage == stages) {
+      at.stage = 0;
+      at.phase ^= 1u;
+    }
+    if (k + 1 < kblocks) ready = mbar_try_wait(&full[at.stage], at.phase);
+    if (elect_one()) {
+      const uint32_t w = base + static_cast<uint32_t>(stage) * (stage_bytes >> 4);
+      const uint32_t x = w + (kI8WBytes >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kI8K / 32; ++kk)
+        mma(high | (w + kk * 2), high | (x + kk * 2), (k > 0 || kk > 0) ? 1u : 0u);
+      commit(stage);
+    }
+    __syncwarp();
+  }
+  return true;
+}
+
 // This thread's channel of y: what its columns are scaled and stored with.
 // All lanes of a warp call put together (its pairs of lanes exchange values).
 template <typename O>
@@ -418,28 +465,14 @@ __global__ void __launch_bounds__(kTileI8Threads)
       mbar_wait(&tail.full[j % P.stages], static_cast<uint32_t>((j / P.stages) & 1),
                 kDrainTimeoutNs, nullptr);
   } else if (warp == 1) {
-    int stage = 0;
-    uint32_t phase = 0;
-    for (int k = kb0; k < kb1; ++k) {
-      if (!i8_wait(&tail.full[stage], phase, timeout_ns, abort_flag)) {
-        linear_give_up(abort_flag);
-        break;
-      }
-      tc_fence_after_sync();
-      if (elect_one()) {
-        const uint32_t w = smem_addr(ring + stage * stage_bytes), x = w + kI8WBytes;
-#pragma unroll
-        for (int kk = 0; kk < kI8K / 32; ++kk)
-          umma_i8(tmem, sw128_kmajor_desc(w + kk * 32), sw128_kmajor_desc(x + kk * 32), P.idesc,
-                  (k > kb0 || kk > 0) ? 1u : 0u);
-        umma_commit(&tail.empty[stage]);
-      }
-      __syncwarp();
-      if (++stage == P.stages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
+    I8Stage at{0, 0};
+    i8_mma_loop(
+        kb1 - kb0, P.stages, smem_addr(ring), stage_bytes, tail.full, at, timeout_ns, abort_flag,
+        [&](uint64_t w, uint64_t x, uint32_t accumulate) {
+          umma_i8(tmem, w, x, P.idesc, accumulate);
+        },
+        [&](int stage) { umma_commit(&tail.empty[stage]); },
+        [&] { linear_give_up(abort_flag); });
     // Also after a give-up: completes once the issued MMAs have.
     if (elect_one()) umma_commit(&tail.acc);
     __syncwarp();
@@ -626,8 +659,8 @@ __global__ void __launch_bounds__(kPairI8Threads)
   } else if (warp == kPairI8EpiWarps + 1) {
     // ------------------------------------------------------------- MMA issuer
     if (half == 0) {
-      int stage = 0, it = 0;
-      uint32_t phase = 0;
+      I8Stage at{0, 0};
+      int it = 0;
       bool ok = true;
       for (int i = first; ok && i < tiles; i += step, ++it) {
         const int b = it & 1;
@@ -638,27 +671,13 @@ __global__ void __launch_bounds__(kPairI8Threads)
         }
         tc_fence_after_sync();
         const uint32_t d = tmem + static_cast<uint32_t>(b * kI8MaxN);
-        for (int k = kb0; k < kb1; ++k) {
-          if (!i8_wait(&tail.full[stage], phase, timeout_ns, abort_flag)) {
-            give_up();
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          if (elect_one()) {
-            const uint32_t w = smem_addr(ring + stage * stage_bytes), x = w + kI8WBytes;
-#pragma unroll
-            for (int kk = 0; kk < kI8K / 32; ++kk)
-              umma_i8_pair(d, sw128_kmajor_desc(w + kk * 32), sw128_kmajor_desc(x + kk * 32),
-                           P.idesc, (k > kb0 || kk > 0) ? 1u : 0u);
-            umma_commit_pair(&tail.empty[stage], pair_mask);
-          }
-          __syncwarp();
-          if (++stage == P.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
+        ok = i8_mma_loop(
+            kb1 - kb0, P.stages, smem_addr(ring), stage_bytes, tail.full, at, timeout_ns,
+            abort_flag,
+            [&](uint64_t w, uint64_t x, uint32_t accumulate) {
+              umma_i8_pair(d, w, x, P.idesc, accumulate);
+            },
+            [&](int stage) { umma_commit_pair(&tail.empty[stage], pair_mask); }, give_up);
         if (elect_one()) umma_commit_pair(&tail.acc_full[b], pair_mask);
         __syncwarp();
       }
