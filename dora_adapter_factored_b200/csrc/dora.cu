@@ -2177,6 +2177,31 @@ LinearPlan plan_linear(int T, int d_out, int d_in, int sms) {
   return p;
 }
 
+// The ring of k-block stages in `room` bytes of shared memory, and the partials
+// of a split k: behind a ring of at least four stages (or all k-blocks), else
+// over the ring, at the price of a cluster barrier before they are written.
+struct I8Ring {
+  int stages;
+  uint32_t part_off;
+  bool part_over_ring;
+  size_t bytes;
+};
+
+I8Ring plan_i8_ring(size_t room, size_t stage, const LinearPlan& p) {
+  const size_t part = i8_partial_bytes(p.n, p.splits);
+  // (a persistent pair's ring runs on into its next tile)
+  const size_t most = p.pair && p.splits == 1
+                          ? size_t(kI8MaxStages)
+                          : std::min<size_t>(kI8MaxStages, ceil_div_ll(p.kb, p.splits));
+  I8Ring r;
+  r.part_over_ring = part + std::min<size_t>(most, 4) * stage > room;
+  r.stages = static_cast<int>(std::min(most, (room - (r.part_over_ring ? 0 : part)) / stage));
+  const size_t ring = r.stages * stage;
+  r.part_off = r.part_over_ring ? 0 : static_cast<uint32_t>(ring);
+  r.bytes = r.part_over_ring ? std::max(ring, part) : ring + part;
+  return r;
+}
+
 template <typename O>
 dora_status_t launch_tile_i8(const LinearPlan& p, const LinearArgs& A, const int8_t* xq,
                              const int8_t* wq, int ld, int sms, cudaStream_t cs) {
@@ -2190,19 +2215,14 @@ dora_status_t launch_tile_i8(const LinearPlan& p, const LinearArgs& A, const int
   P.tmem_cols = 32;
   while (P.tmem_cols < static_cast<uint32_t>(p.n)) P.tmem_cols *= 2;
   P.idesc = idesc_i8_s32(kI8M, p.n);
-  // Two CTAs per SM where there are more CTAs than SMs, else one.  The
-  // partials of a split k lie behind the ring up to 32 KiB, else over it.
+  // Two CTAs per SM where there are more CTAs than SMs, else one.
   const long long ctas = static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits;
   const size_t dyn = ctas > sms ? (size_t(113) << 10) - sizeof(TileI8Tail) : kTileI8MaxDynSmem;
-  const size_t part = i8_partial_bytes(p.n, p.splits);
-  P.part_over_ring = part > (size_t(32) << 10);
-  const size_t stage = kI8WBytes + static_cast<size_t>(p.n) * kI8K;
-  const size_t room = dyn - 1024 - (P.part_over_ring ? 0 : part);
-  P.stages = static_cast<int>(std::min<size_t>(
-      {room / stage, size_t(kI8MaxStages), static_cast<size_t>(ceil_div_ll(p.kb, p.splits))}));
-  const size_t ring = P.stages * stage;
-  P.part_off = P.part_over_ring ? 0 : static_cast<uint32_t>(ring);
-  const size_t used = P.part_over_ring ? std::max(ring, part) : ring + part;
+  const I8Ring r = plan_i8_ring(dyn - 1024, kI8WBytes + static_cast<size_t>(p.n) * kI8K, p);
+  P.stages = r.stages;
+  P.part_off = r.part_off;
+  P.part_over_ring = r.part_over_ring;
+  const size_t used = r.bytes;
   const size_t smem = std::max(used + 1024, tmem_smem_floor(P.tmem_cols) - sizeof(TileI8Tail));
   const dim3 grid(p.tiles_m * p.splits, p.tiles_n);
   const unsigned long long to = g_timeout_ns.load();
@@ -2237,9 +2257,11 @@ dora_status_t launch_pair_i8(const LinearPlan& p, const LinearArgs& A, const int
   P.group = static_cast<int>(std::max<size_t>(
       1, std::min<size_t>(p.tiles_n, kPairI8GroupBytes / (static_cast<size_t>(p.n) * ld))));
   P.idesc = idesc_i8_s32(2 * kI8M, p.n);
-  const size_t stage = kI8WBytes + static_cast<size_t>(p.n / 2) * kI8K;
-  P.stages = static_cast<int>(
-      std::min<size_t>((kPairI8MaxDynSmem - 1024) / stage, size_t(kI8MaxStages)));
+  const I8Ring r = plan_i8_ring(kPairI8MaxDynSmem - 1024,
+                                kI8WBytes + static_cast<size_t>(p.n / 2) * kI8K, p);
+  P.stages = r.stages;
+  P.part_off = r.part_off;
+  P.part_over_ring = r.part_over_ring;
   const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
   const long long clusters = p.splits > 1 ? tiles : std::min<long long>(tiles, sms / 2);
   const unsigned long long to = g_timeout_ns.load();

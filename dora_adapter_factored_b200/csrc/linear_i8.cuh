@@ -154,9 +154,9 @@ __global__ void __launch_bounds__(kDotWarps * 32) dot_i8_kernel(const LinearArgs
 // accumulator in TMEM (lane = channel, column = token).
 //
 // Where the tiles alone would leave SMs idle, S CTAs (or pairs) of a cluster
-// share a tile's k.  Each finishes n / S of the tile's columns: the others
-// push their partials of those columns into its shared memory, each thread
-// four columns of its channel per store (scalar stores, or pulling the
+// share a tile's k.  Each finishes n / S of the tile's columns from its own
+// accumulator and from what the others push into its shared memory, each
+// thread four columns of its channel per store (scalar stores, or pulling the
 // partials, cost the remote latency or the address arithmetic per column).
 constexpr int kI8M = 128;  // channels per CTA (TMEM lanes)
 constexpr int kI8K = 128;  // codes per k-block: one 128-byte swizzle row
@@ -285,50 +285,61 @@ struct ChannelOut {
   }
 };
 
-// Calls f(c, v) with the n accumulator columns (a multiple of 16) from `tmem`,
-// 16 at a time, the next 16 on their way meanwhile.
+// Epilogue warps of a CTA: two per quarter of the TMEM lanes (a warp reads the
+// quarter of its index modulo 4), which take the 16-column groups in turn.
+constexpr int kI8EpiWarps = 8;
+
+// Calls f(c, v) with this warp's groups of 16 among the n accumulator columns
+// (a multiple of 16) from `tmem`, the next group on its way meanwhile.
 template <typename F>
-__device__ __forceinline__ void for_columns(uint32_t tmem, int n, F&& f) {
+__device__ __forceinline__ void for_columns(uint32_t tmem, int n, int warp, F&& f) {
+  int c = (warp >> 2) * 16;
+  if (c >= n) return;
   int a[16], b[16];
-  tmem_load_16cols(tmem, a);
-  for (int c = 0; c < n; c += 32) {
+  tmem_load_16cols(tmem + c, a);
+  for (; c < n; c += 64) {
     tmem_wait_16cols(a);
-    if (c + 16 < n) tmem_load_16cols(tmem + c + 16, b);
+    if (c + 32 < n) tmem_load_16cols(tmem + c + 32, b);
     f(c, a);
     __syncwarp();
-    if (c + 16 < n) {
+    if (c + 32 < n) {
       tmem_wait_16cols(b);
-      if (c + 32 < n) tmem_load_16cols(tmem + c + 32, a);
-      f(c + 16, b);
+      if (c + 64 < n) tmem_load_16cols(tmem + c + 64, a);
+      f(c + 32, b);
       __syncwarp();
     }
   }
 }
 
-// Partials of a split k in a CTA: [S][128 channels][n / S columns, padded by
-// one 16-byte step against bank conflicts] int32.
+// Partials of a split k in the CTA that sums them: [S - 1 other slices][128
+// channels][n / S columns, padded by one 16-byte step against bank conflicts]
+// int32.
 __host__ __device__ constexpr uint32_t i8_partial_stride(int n, int S) { return n / S + 4; }
 __host__ __device__ constexpr uint32_t i8_partial_bytes(int n, int S) {
-  return S > 1 ? static_cast<uint32_t>(S) * kI8M * i8_partial_stride(n, S) * 4u : 0u;
+  return static_cast<uint32_t>(S - 1) * kI8M * i8_partial_stride(n, S) * 4u;
 }
 
-// Threads 0-127: pushes this CTA's accumulator columns to the CTAs that finish
-// them.  `slice`: this CTA's share of k; the CTA of slice s has cluster rank
-// s * rank_step + rank_off.  n is a multiple of 16 and n / S of 4.
+// Epilogue warps: pushes the columns that other CTAs finish to them.  `slice`:
+// this CTA's share of k; the CTA of slice s has cluster rank s * rank_step +
+// rank_off.  n is a multiple of 16 and n / S of 4.
 template <int S>
-__device__ __forceinline__ void i8_push_partials(uint32_t lane_base, int n, int slice,
-                                                 int rank_step, int rank_off, const int* part) {
+__device__ __forceinline__ void i8_push_partials(uint32_t lane_base, int n, int warp, int lane,
+                                                 int slice, int rank_step, int rank_off,
+                                                 const int* part) {
   const int cols = n / S;
-  const uint32_t stride = i8_partial_stride(n, S);
+  const uint32_t stride = i8_partial_stride(n, S) * 4u;
   const uint32_t mine =
-      smem_addr(part) + (static_cast<uint32_t>(slice) * kI8M + threadIdx.x) * stride * 4u;
-  int owner = 0, in = 0;  // of the next four columns
-  for_columns(lane_base, n, [&](int, const int(&v)[16]) {
+      smem_addr(part) + static_cast<uint32_t>((warp & 3) * 32 + lane) * stride;
+  for_columns(lane_base, n, warp, [&](int c0, const int(&v)[16]) {
+    int owner = c0 / cols, in = c0 - owner * cols;  // of the next four columns
 #pragma unroll
     for (int q = 0; q < 16; q += 4) {
-      st_cluster_v4(mapa_shared(mine + static_cast<uint32_t>(in) * 4u,
-                                static_cast<uint32_t>(owner * rank_step + rank_off)),
-                    v[q], v[q + 1], v[q + 2], v[q + 3]);
+      if (owner != slice) {
+        const uint32_t from = static_cast<uint32_t>(slice < owner ? slice : slice - 1);
+        st_cluster_v4(mapa_shared(mine + from * kI8M * stride + static_cast<uint32_t>(in) * 4u,
+                                  static_cast<uint32_t>(owner * rank_step + rank_off)),
+                      v[q], v[q + 1], v[q + 2], v[q + 3]);
+      }
       in += 4;
       if (in == cols) {
         in = 0;
@@ -338,40 +349,50 @@ __device__ __forceinline__ void i8_push_partials(uint32_t lane_base, int n, int 
   });
 }
 
-// Threads 0-127: sums and stores this CTA's columns of the tile at token t0.
+// Epilogue warps: adds the others' partials to this CTA's own columns of the
+// tile at token t0 and stores them.
 template <int S, typename O>
-__device__ __forceinline__ void i8_finish_columns(const ChannelOut<O>& out, const float* sx, int n,
+__device__ __forceinline__ void i8_finish_columns(const ChannelOut<O>& out, const float* sx,
+                                                  uint32_t lane_base, int n, int warp, int lane,
                                                   int slice, int t0, const int* part) {
   const int cols = n / S;
-  const int* p = part + threadIdx.x * i8_partial_stride(n, S);
+  const int* p = part + ((warp & 3) * 32 + lane) * i8_partial_stride(n, S);
   const uint32_t from = kI8M * i8_partial_stride(n, S);  // to the next slice's partials
-  auto group = [&](auto width, int c) {
-    constexpr int N = decltype(width)::value;
-    int sum[N];
+  auto group = [&](auto& sum, int c) {
+    constexpr int N = sizeof(sum) / sizeof(int);
 #pragma unroll
     for (int e = 0; e < N; e += 4) {
-      int4 v[S];
+      int4 v[S - 1];
 #pragma unroll
-      for (int s = 0; s < S; ++s) v[s] = *reinterpret_cast<const int4*>(p + s * from + c + e);
-      sum[e] = sum[e + 1] = sum[e + 2] = sum[e + 3] = 0;
+      for (int s = 0; s < S - 1; ++s) v[s] = *reinterpret_cast<const int4*>(p + s * from + c + e);
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
+      for (int s = 0; s < S - 1; ++s) {
         sum[e] += v[s].x; sum[e + 1] += v[s].y; sum[e + 2] += v[s].z; sum[e + 3] += v[s].w;
       }
     }
-    const int at = slice * cols + c;
-    out.put(t0 + at, sum, sx + at);
+    out.put(t0 + slice * cols + c, sum, sx + slice * cols + c);
+    __syncwarp();
   };
-  int c = 0;
-  for (; c + 16 <= cols; c += 16) group(std::integral_constant<int, 16>(), c);
-  for (; c < cols; c += 4) group(std::integral_constant<int, 4>(), c);
+  const uint32_t own = lane_base + static_cast<uint32_t>(slice * cols);
+  const int whole = cols & ~15;
+  for (int c = (warp >> 2) * 16; c < whole; c += 32) {
+    int sum[16];
+    tmem_load_16cols(own + c, sum);
+    tmem_wait_16cols(sum);
+    group(sum, c);
+  }
+  for (int c = whole + (warp >> 2) * 4; c < cols; c += 8) {
+    int sum[4];
+    tmem_load_4cols_wait(own + c, sum);
+    group(sum, c);
+  }
 }
 
 // ------------------------------------------------ single CTAs: small batches
 // One tile of 128 channels by up to 256 tokens per CTA.  Not persistent: with
 // up to 113 KiB and 256 TMEM columns per CTA two CTAs share an SM, so one's
 // epilogue runs beside the other's stream.
-constexpr int kTileI8Threads = 128;
+constexpr int kTileI8Threads = kI8EpiWarps * 32;
 
 struct alignas(64) TileI8Dev {
   CUtensorMap tm_w;  // wq [d_out, ld], box 128 x 128
@@ -478,17 +499,17 @@ __global__ void __launch_bounds__(kTileI8Threads)
     __syncwarp();
     mbar_wait(&tail.acc, 0, kDrainTimeoutNs, nullptr);
   } else {
-    for (int c = static_cast<int>(threadIdx.x) - 64; c < P.n; c += 64)
+    for (int c = static_cast<int>(threadIdx.x) - 64; c < P.n; c += kTileI8Threads - 64)
       tail.sx[c] = t0 + c < P.a.T ? P.a.x_scale[t0 + c] : 0.f;
   }
   __syncwarp();
   if (!mbar_wait_fast(&tail.acc, 0, timeout_ns, abort_flag)) linear_give_up(abort_flag);
   __syncthreads();  // every wait is over, sx is written
   tc_fence_after_sync();
-  const ChannelOut<O> out(P.a, row0 + static_cast<int>(threadIdx.x), *abort_flag == 0);
-  const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  const ChannelOut<O> out(P.a, row0 + (warp & 3) * 32 + lane, *abort_flag == 0);
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   if constexpr (S == 1) {
-    for_columns(lane_base, P.n,
+    for_columns(lane_base, P.n, warp,
                 [&](int c, const int(&v)[16]) { out.put(t0 + c, v, tail.sx + c); });
   } else {
     // Behind the ring, or over it once every CTA's copies have landed and its
@@ -498,9 +519,9 @@ __global__ void __launch_bounds__(kTileI8Threads)
       cluster_sync();
     }
     const int* part = reinterpret_cast<const int*>(ring + P.part_off);
-    i8_push_partials<S>(lane_base, P.n, slice, 1, 0, part);
+    i8_push_partials<S>(lane_base, P.n, warp, lane, slice, 1, 0, part);
     cluster_sync();
-    i8_finish_columns<S>(out, tail.sx, P.n, slice, t0, part);
+    i8_finish_columns<S>(out, tail.sx, lane_base, P.n, warp, lane, slice, t0, part);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -520,8 +541,7 @@ __global__ void __launch_bounds__(kTileI8Threads)
 // S == 1: persistent, over all tiles, with two accumulators of 256 columns so
 // that a tile's epilogue runs beside the next one's MMAs.  S > 1: one tile per
 // cluster of S pairs, which share its k.
-constexpr int kPairI8EpiWarps = 4;
-constexpr int kPairI8Threads = (kPairI8EpiWarps + 2) * 32;  // + copies, + MMA
+constexpr int kPairI8Threads = (kI8EpiWarps + 2) * 32;  // + copies, + MMA
 
 struct alignas(64) PairI8Dev {
   CUtensorMap tm_w;  // wq [d_out, ld], box 128 x 128
@@ -531,6 +551,8 @@ struct alignas(64) PairI8Dev {
   int kb;            // k-blocks
   int stages;
   int tiles_m, tiles_n, group;  // `group` token tiles go together, channels outside
+  uint32_t part_off;            // of the partials, from the ring's start
+  int part_over_ring;
   uint32_t idesc;
 };
 
@@ -545,7 +567,7 @@ struct PairI8Tail {
   uint64_t empty[kI8MaxStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
-  alignas(16) float sx[kPairI8EpiWarps][kI8MaxN];  // a tile's token scales, per epilogue warp
+  alignas(16) float sx[2][kI8MaxN];  // a tile's token scales, one copy per accumulator
   uint32_t tmem_slot;
   int abort_flag;
 };
@@ -579,6 +601,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
   const int kb1 = static_cast<int>(static_cast<long long>(slice + 1) * P.kb / S);
   const uint32_t stage_bytes = kI8WBytes + static_cast<uint32_t>(P.n / 2) * kI8K;
   const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
+  const int chan = static_cast<int>(half) * kI8M + (warp & 3) * 32 + lane;  // in the tile
   const int tiles = P.tiles_m * P.tiles_n;
   const int first = static_cast<int>(blockIdx.x) / (2 * S);
   const int step = static_cast<int>(gridDim.x) / (2 * S);
@@ -594,7 +617,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tail.acc_full[b], 1);
-      mbar_init(&tail.acc_empty[b], 2 * kPairI8EpiWarps);
+      mbar_init(&tail.acc_empty[b], 2 * kI8EpiWarps);
     }
     mbar_init(&tail.drain, 1);
     tail.abort_flag = 0;
@@ -611,10 +634,11 @@ __global__ void __launch_bounds__(kPairI8Threads)
   cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = tail.tmem_slot;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   grid_dependency_wait();
   grid_dependency_trigger();  // not before TMEM is held: the next grid may want it too
 
-  if (warp == kPairI8EpiWarps) {
+  if (warp == kI8EpiWarps) {
     // ---------------------------------------------------------- copy producer
     const uint64_t pol = policy_evict_last();
     const uint32_t full0 = mapa_shared(smem_addr(&tail.full[0]), lead);
@@ -656,7 +680,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
       mbar_wait(half == 0 ? &tail.full[j % P.stages] : &tail.empty[j % P.stages], par,
                 kDrainTimeoutNs, nullptr);
     }
-  } else if (warp == kPairI8EpiWarps + 1) {
+  } else if (warp == kI8EpiWarps + 1) {
     // ------------------------------------------------------------- MMA issuer
     if (half == 0) {
       I8Stage at{0, 0};
@@ -687,32 +711,31 @@ __global__ void __launch_bounds__(kPairI8Threads)
       mbar_wait(&tail.drain, 0, kDrainTimeoutNs, nullptr);
     }
   } else {
-    // ---------------------------------------------------- epilogue (warps 0-3)
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    // ---------------------------------------------------- epilogue (warps 0-7)
     const uint32_t empty0 = mapa_shared(smem_addr(&tail.acc_empty[0]), lead);
-    float* sx = tail.sx[S == 1 ? warp : 0];
     int it = 0;
     for (int i = first; i < tiles; i += step, ++it) {
       int tm, tn;
       pair_tile(P, i, tm, tn);
       const int b = it & 1, t0 = tn * P.n;
-      const int row = tm * 2 * kI8M + static_cast<int>(half) * kI8M + warp * 32 + lane;
-      // Each warp its own copy of the scales (S == 1), or one for the CTA.
-      for (int c = S == 1 ? lane : static_cast<int>(threadIdx.x); c < P.n; c += S == 1 ? 32 : 128)
+      // The scales' copy of this accumulator: a warp is back here with the same
+      // one two tiles on, past a barrier that every warp reached after reading
+      // it.  No warp leaves the loop early, so each barrier completes.
+      float* sx = tail.sx[b];
+      for (int c = static_cast<int>(threadIdx.x); c < P.n; c += kI8EpiWarps * 32)
         sx[c] = t0 + c < P.a.T ? P.a.x_scale[t0 + c] : 0.f;
-      __syncwarp();
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait_fast(&tail.acc_full[b], static_cast<uint32_t>((it >> 1) & 1),
-                                timeout_ns, abort_flag))) {
+      named_barrier_sync(1, kI8EpiWarps * 32);
+      if (!i8_wait(&tail.acc_full[b], static_cast<uint32_t>((it >> 1) & 1), timeout_ns,
+                   abort_flag)) {
         give_up();
-        break;
+        continue;
       }
       tc_fence_after_sync();
       if constexpr (S == 1) {
-        const ChannelOut<O> out(P.a, row, *abort_flag == 0);
+        const ChannelOut<O> out(P.a, tm * 2 * kI8M + chan, *abort_flag == 0);
         const uint32_t acc = lane_base + static_cast<uint32_t>(b * kI8MaxN);
-        for_columns(acc, P.n, [&](int c, const int(&v)[16]) {
-          if (c + 16 == P.n) {  // the last columns are in registers: hand it back
+        for_columns(acc, P.n, warp, [&](int c, const int(&v)[16]) {
+          if (c + 32 >= P.n) {  // this warp's last columns are in registers: hand it back
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
@@ -724,32 +747,29 @@ __global__ void __launch_bounds__(kPairI8Threads)
     }
   }
   if constexpr (S > 1) {
-    // The one tile's partials, over the ring: no copy or MMA of any CTA of the
-    // cluster is in flight past the first barrier.
+    // The one tile's partials: behind the ring, or over it once no copy or MMA
+    // of any CTA of the cluster is in flight.
     int tm, tn;
     pair_tile(P, first, tm, tn);
-    const int t0 = tn * P.n;
-    const int* part = reinterpret_cast<const int*>(ring);
+    const int* part = reinterpret_cast<const int*>(ring + P.part_off);
     __syncwarp();
     tc_fence_before_sync();
-    cluster_sync();
+    if (P.part_over_ring) cluster_sync();
     tc_fence_after_sync();
-    if (warp < kPairI8EpiWarps)
-      i8_push_partials<S>(tmem + (static_cast<uint32_t>(warp * 32) << 16), P.n, slice, 2,
-                          static_cast<int>(half), part);
+    if (warp < kI8EpiWarps)
+      i8_push_partials<S>(lane_base, P.n, warp, lane, slice, 2, static_cast<int>(half), part);
     __syncwarp();
     cluster_sync();
-    if (warp < kPairI8EpiWarps) {
-      const ChannelOut<O> out(P.a, tm * 2 * kI8M + static_cast<int>(half) * kI8M + threadIdx.x,
-                              *abort_flag == 0);
-      i8_finish_columns<S>(out, tail.sx[0], P.n, slice, t0, part);
+    if (warp < kI8EpiWarps) {
+      const ChannelOut<O> out(P.a, tm * 2 * kI8M + chan, *abort_flag == 0);
+      i8_finish_columns<S>(out, tail.sx[0], lane_base, P.n, warp, lane, slice, tn * P.n, part);
     }
   }
   // Neither CTA leaves (or frees TMEM) while the other may still signal it or
   // read its shared memory through the MMAs.
   __syncwarp();
   tc_fence_before_sync();
-  cluster_sync();
+  cluster_sync_relaxed();
   if (warp == 0) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem, 512);

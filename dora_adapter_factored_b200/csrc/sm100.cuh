@@ -484,6 +484,28 @@ __device__ __forceinline__ void tmem_wait_16cols(int (&v)[16]) {
                : "memory");
 }
 
+// As the two above, 4 columns, landed.
+__device__ __forceinline__ void tmem_load_4cols_wait(uint32_t taddr, int (&v)[4]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Barrier `id` (1 .. 15) of the block, for `threads` of its threads.
+__device__ __forceinline__ void named_barrier_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Every thread of the cluster, ordering no memory accesses: for CTAs that only
+// must not leave before the others are done.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\t"
+               "barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                              uint32_t idesc, uint32_t accumulate) {
   asm volatile(
