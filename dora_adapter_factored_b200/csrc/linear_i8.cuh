@@ -155,9 +155,7 @@ __global__ void __launch_bounds__(kDotWarps * 32) dot_i8_kernel(const LinearArgs
 //
 // Where the tiles alone would leave SMs idle, S CTAs (or pairs) of a cluster
 // share a tile's k.  Each finishes n / S of the tile's columns from its own
-// accumulator and from what the others push into its shared memory, each
-// thread four columns of its channel per store (scalar stores, or pulling the
-// partials, cost the remote latency or the address arithmetic per column).
+// accumulator and from what the others push into its shared memory.
 constexpr int kI8M = 128;  // channels per CTA (TMEM lanes)
 constexpr int kI8K = 128;  // codes per k-block: one 128-byte swizzle row
 constexpr int kI8MaxN = 256;
@@ -232,8 +230,9 @@ struct ChannelOut {
   bool pairs;  // bf16: channels 2i and 2i + 1 are stored together, 4 bytes aligned
   int T;
   long long d_out;
-  __device__ __forceinline__ ChannelOut(const LinearArgs& a, int row, bool may_store) {
-    ok = may_store && row < a.d_out && DORA_BOUNDS_OK(row >= 0);
+  // (made before the accumulator is waited for: the scale comes from memory)
+  __device__ __forceinline__ ChannelOut(const LinearArgs& a, int row) {
+    ok = row < a.d_out && DORA_BOUNDS_OK(row >= 0);
     has_bias = a.bias != nullptr;
     pairs = sizeof(O) == 2 && a.d_out % 2 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 3) == 0;
     y = static_cast<O*>(a.y) + (pairs ? row & ~1 : row);
@@ -311,12 +310,11 @@ __device__ __forceinline__ void for_columns(uint32_t tmem, int n, int warp, F&& 
   }
 }
 
-// Partials of a split k in the CTA that sums them: [S - 1 other slices][128
-// channels][n / S columns, padded by one 16-byte step against bank conflicts]
-// int32.
-__host__ __device__ constexpr uint32_t i8_partial_stride(int n, int S) { return n / S + 4; }
+// Partials of a split k in the CTA that sums them: [S - 1 other slices][n / S
+// columns][128 channels] int32, so that a warp's store of one column is 128
+// consecutive bytes.
 __host__ __device__ constexpr uint32_t i8_partial_bytes(int n, int S) {
-  return static_cast<uint32_t>(S - 1) * kI8M * i8_partial_stride(n, S) * 4u;
+  return static_cast<uint32_t>(S - 1) * static_cast<uint32_t>(n / S) * kI8M * 4u;
 }
 
 // Epilogue warps: pushes the columns that other CTAs finish to them.  `slice`:
@@ -327,18 +325,19 @@ __device__ __forceinline__ void i8_push_partials(uint32_t lane_base, int n, int 
                                                  int slice, int rank_step, int rank_off,
                                                  const int* part) {
   const int cols = n / S;
-  const uint32_t stride = i8_partial_stride(n, S) * 4u;
-  const uint32_t mine =
-      smem_addr(part) + static_cast<uint32_t>((warp & 3) * 32 + lane) * stride;
+  const uint32_t mine = smem_addr(part) + static_cast<uint32_t>((warp & 3) * 32 + lane) * 4u;
   for_columns(lane_base, n, warp, [&](int c0, const int(&v)[16]) {
     int owner = c0 / cols, in = c0 - owner * cols;  // of the next four columns
 #pragma unroll
     for (int q = 0; q < 16; q += 4) {
       if (owner != slice) {
-        const uint32_t from = static_cast<uint32_t>(slice < owner ? slice : slice - 1);
-        st_cluster_v4(mapa_shared(mine + from * kI8M * stride + static_cast<uint32_t>(in) * 4u,
-                                  static_cast<uint32_t>(owner * rank_step + rank_off)),
-                      v[q], v[q + 1], v[q + 2], v[q + 3]);
+        const int from = slice < owner ? slice : slice - 1;
+        const uint32_t to = mapa_shared(
+            mine + static_cast<uint32_t>((from * cols + in) * kI8M) * 4u,
+            static_cast<uint32_t>(owner * rank_step + rank_off));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          st_cluster_u32(to + static_cast<uint32_t>(e * kI8M * 4), static_cast<uint32_t>(v[q + e]));
       }
       in += 4;
       if (in == cols) {
@@ -356,20 +355,13 @@ __device__ __forceinline__ void i8_finish_columns(const ChannelOut<O>& out, cons
                                                   uint32_t lane_base, int n, int warp, int lane,
                                                   int slice, int t0, const int* part) {
   const int cols = n / S;
-  const int* p = part + ((warp & 3) * 32 + lane) * i8_partial_stride(n, S);
-  const uint32_t from = kI8M * i8_partial_stride(n, S);  // to the next slice's partials
+  const int* p = part + (warp & 3) * 32 + lane;
   auto group = [&](auto& sum, int c) {
     constexpr int N = sizeof(sum) / sizeof(int);
 #pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      int4 v[S - 1];
+    for (int s = 0; s < S - 1; ++s)
 #pragma unroll
-      for (int s = 0; s < S - 1; ++s) v[s] = *reinterpret_cast<const int4*>(p + s * from + c + e);
-#pragma unroll
-      for (int s = 0; s < S - 1; ++s) {
-        sum[e] += v[s].x; sum[e + 1] += v[s].y; sum[e + 2] += v[s].z; sum[e + 3] += v[s].w;
-      }
-    }
+      for (int e = 0; e < N; ++e) sum[e] += p[(s * cols + c + e) * kI8M];
     out.put(t0 + slice * cols + c, sum, sx + slice * cols + c);
     __syncwarp();
   };
@@ -503,10 +495,11 @@ __global__ void __launch_bounds__(kTileI8Threads)
       tail.sx[c] = t0 + c < P.a.T ? P.a.x_scale[t0 + c] : 0.f;
   }
   __syncwarp();
+  ChannelOut<O> out(P.a, row0 + (warp & 3) * 32 + lane);
   if (!mbar_wait_fast(&tail.acc, 0, timeout_ns, abort_flag)) linear_give_up(abort_flag);
   __syncthreads();  // every wait is over, sx is written
   tc_fence_after_sync();
-  const ChannelOut<O> out(P.a, row0 + (warp & 3) * 32 + lane, *abort_flag == 0);
+  if (*abort_flag != 0) out.ok = false;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   if constexpr (S == 1) {
     for_columns(lane_base, P.n, warp,
@@ -722,6 +715,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
       // one two tiles on, past a barrier that every warp reached after reading
       // it.  No warp leaves the loop early, so each barrier completes.
       float* sx = tail.sx[b];
+      ChannelOut<O> out(P.a, tm * 2 * kI8M + chan);
       for (int c = static_cast<int>(threadIdx.x); c < P.n; c += kI8EpiWarps * 32)
         sx[c] = t0 + c < P.a.T ? P.a.x_scale[t0 + c] : 0.f;
       named_barrier_sync(1, kI8EpiWarps * 32);
@@ -732,7 +726,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
       }
       tc_fence_after_sync();
       if constexpr (S == 1) {
-        const ChannelOut<O> out(P.a, tm * 2 * kI8M + chan, *abort_flag == 0);
+        if (*abort_flag != 0) out.ok = false;
         const uint32_t acc = lane_base + static_cast<uint32_t>(b * kI8MaxN);
         for_columns(acc, P.n, warp, [&](int c, const int(&v)[16]) {
           if (c + 32 >= P.n) {  // this warp's last columns are in registers: hand it back
@@ -752,6 +746,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
     int tm, tn;
     pair_tile(P, first, tm, tn);
     const int* part = reinterpret_cast<const int*>(ring + P.part_off);
+    ChannelOut<O> out(P.a, tm * 2 * kI8M + chan);
     __syncwarp();
     tc_fence_before_sync();
     if (P.part_over_ring) cluster_sync();
@@ -761,7 +756,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
     __syncwarp();
     cluster_sync();
     if (warp < kI8EpiWarps) {
-      const ChannelOut<O> out(P.a, tm * 2 * kI8M + chan, *abort_flag == 0);
+      if (*abort_flag != 0) out.ok = false;
       i8_finish_columns<S>(out, tail.sx[0], lane_base, P.n, warp, lane, slice, tn * P.n, part);
     }
   }
