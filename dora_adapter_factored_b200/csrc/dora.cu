@@ -65,6 +65,8 @@ struct DeviceInfo {
   int sms = 0;
   bool attrs_set = false;
   int norm_pairs = 0;  // CTA pairs of the norm GEMM resident at once
+  int clusters4 = 0;   // clusters of 4 and of 8 CTAs, one CTA per SM, resident at once
+  int clusters8 = 0;
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
@@ -730,6 +732,31 @@ cudaError_t linear_smem_attrs() {
   return e;
 }
 
+// Clusters of `size` CTAs of the split 8-bit product that can be resident at
+// once with one CTA per SM (fewer than sms / size: a cluster stays inside a
+// GPC).
+int resident_clusters(unsigned size, int sms) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(kTileI8Threads);
+  cfg.dynamicSmemBytes = kTileI8MaxDynSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const cudaError_t e =
+      size == 4 ? cudaOccupancyMaxActiveClusters(&n, tile_i8_kernel<float, 4>, &cfg)
+                : cudaOccupancyMaxActiveClusters(&n, tile_i8_kernel<float, 8>, &cfg);
+  if (e != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = std::max(1, sms / static_cast<int>(size));
+  }
+  return n;
+}
+
 bool ensure_tc_attrs() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
@@ -766,6 +793,8 @@ bool ensure_tc_attrs() {
     clusters = std::max(1, sms / 2);
   }
   d.norm_pairs = std::min(clusters, std::max(1, sms / 2));
+  d.clusters4 = resident_clusters(4, sms);
+  d.clusters8 = resident_clusters(8, sms);
   d.attrs_set = true;
   return true;
 }
@@ -2105,8 +2134,8 @@ void launch_dot_any(const LinearArgs& P, bool vec, int sms, cudaStream_t cs) {
     launch_dot<O, kDotTokens>(P, vec, sms, cs);
 }
 
-// The dot-product kernel up to this many tokens, the tensor cores above.
-constexpr int kDotMaxT = 8;
+// The most tokens the dot-product kernel takes where the tensor cores could.
+constexpr int kDotMaxT = kDotTokens;
 
 int padded_k(int64_t d_in) { return static_cast<int>(align_up(static_cast<size_t>(d_in), 16)); }
 
@@ -2160,21 +2189,92 @@ struct LinearPlan {
   int n, tiles_m, tiles_n, splits, kb;
 };
 
-LinearPlan plan_linear(int T, int d_out, int d_in, int sms) {
-  LinearPlan p;
-  p.pair = T > 64;
-  p.tiles_n = static_cast<int>(ceil_div_ll(T, kI8MaxN));
-  p.n = round_up_int(static_cast<int>(ceil_div_ll(T, p.tiles_n)), p.pair ? 32 : 16);
-  p.tiles_m = static_cast<int>(ceil_div_ll(d_out, p.pair ? 2 * kI8M : kI8M));
-  p.kb = static_cast<int>(ceil_div_ll(d_in, kI8K));
-  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
-  const int units = p.pair ? sms / 2 : sms;
-  p.splits = 1;
-  while (p.splits < (p.pair ? 4 : 8) && tiles * p.splits * 2 <= units &&
-         p.kb >= p.splits * 2 * 4)
-    p.splits *= 2;
-  if (p.splits == 8) p.n = round_up_int(p.n, 32);  // n / splits in steps of four columns
-  return p;
+// Two CTAs share an SM where there are more CTAs than SMs, and where a CTA has
+// few k-blocks, so that the next launch can set itself up beside it (24 tokens
+// at 4096 x 4096, split four ways: 5.8 us against 6.9 us).
+constexpr int kTileI8ShortK = 8;
+bool tile_i8_shares_sm(const LinearPlan& p, int sms) {
+  return static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits > sms ||
+         ceil_div_ll(p.kb, p.splits) <= kTileI8ShortK;
+}
+
+// Estimated time of a plan in us.  What bounds a k-block is the bytes an SM
+// takes in (or their HBM or L2 stream over all CTAs), the MMAs, or the turn of
+// the loop; every plan pays its set-up, the epilogue of its columns and, with a
+// split k, the exchange of partials.  The constants are a fit to the measured
+// times of all plans on 9 weights from 512 x 512 to 25600 x 5120 at 3 to 2048
+// tokens (1000 plans); the plan it picks is on average 1.2 % slower than the
+// fastest of them, where the fixed rule it replaced (pairs above 64 tokens with
+// the widest tile) was 20 % slower.
+double estimate_linear_us(const LinearPlan& p, long long T, long long d_out, long long d_in,
+                          const DeviceInfo& d) {
+  const double n = p.n, S = p.splits;
+  const double tiles = static_cast<double>(p.tiles_m) * p.tiles_n;
+  const double kbs = static_cast<double>(ceil_div_ll(p.kb, p.splits));
+  const double stage_kb = (kI8WBytes + (p.pair ? p.n / 2 : p.n) * kI8K) / 1000.0;
+  const double moved = static_cast<double>(d_out + T) * d_in / 1e6;  // MB from HBM
+  const double exchange = p.splits > 1 ? 0.33 + 0.041 * n * (S - 1) / S : 0.0;
+  const int cluster = (p.pair ? 2 : 1) * p.splits;
+  double slots = cluster == 8   ? d.clusters8
+                 : cluster == 4 ? d.clusters4
+                                : static_cast<double>(d.sms / cluster);
+  double base, kblock, epilogue;
+  if (p.pair) {
+    base = 4.1;
+    kblock = std::max({stage_kb / 147.0, 0.00081 * n, 0.072});
+    epilogue = 0.008 * n / S;
+  } else {
+    const bool two = tiles * S > d.sms;
+    if (two) slots *= 2;
+    const int on_sm = std::min(tiles, slots) * S > d.sms ? 2 : 1;
+    base = 2.35;
+    kblock = std::max({on_sm * stage_kb / (on_sm == 2 ? 98.0 : 147.0), on_sm * 0.00125 * n, 0.18});
+    epilogue = 0.21 + 0.010 * n / S;
+  }
+  const double waves = std::ceil(tiles / slots);
+  const double main = p.pair ? waves * kbs * kblock + epilogue + exchange
+                             : waves * (kbs * kblock + epilogue + exchange);
+  const double l2 = tiles * (p.pair ? 2 : 1) * p.kb * stage_kb / 1000.0;
+  return base + std::max(main, 0.63 + std::max(moved / 6.0, l2 / 17.7));
+}
+
+// The fastest plan by that estimate: a tile of up to 64, 128, 192 or 256
+// tokens, evened out over the token tiles, on one CTA or a pair, with its k
+// whole or split two, four or eight ways.  (One CTA from 17 tokens up to 1024,
+// and tiles of up to 128; beyond, pairs won at every shape.)
+LinearPlan plan_linear(int T, int d_out, int d_in, const DeviceInfo& d, double* us) {
+  LinearPlan best{};
+  *us = 0.0;
+  for (int pair = 0; pair < 2; ++pair)
+    for (int cap = 64; cap <= kI8MaxN; cap += 64) {
+      if (cap > 64 && T <= cap - 64) break;
+      if (pair ? T <= 16 : (cap > 128 || T > 1024)) continue;
+      LinearPlan p;
+      p.pair = pair != 0;
+      p.tiles_n = static_cast<int>(ceil_div_ll(T, cap));
+      p.tiles_m = static_cast<int>(ceil_div_ll(d_out, pair ? 2 * kI8M : kI8M));
+      p.kb = static_cast<int>(ceil_div_ll(d_in, kI8K));
+      for (p.splits = 1; p.splits <= (pair ? 4 : 8) && p.splits <= p.kb; p.splits *= 2) {
+        // n / splits in steps of four columns
+        p.n = round_up_int(static_cast<int>(ceil_div_ll(T, p.tiles_n)),
+                           pair || p.splits == 8 ? 32 : 16);
+        const double t = estimate_linear_us(p, T, d_out, d_in, d);
+        if (best.n == 0 || t < *us) {
+          best = p;
+          *us = t;
+        }
+      }
+    }
+  return best;
+}
+
+// Estimated time of the dot-product kernel: its stream of the weight slows
+// with the tokens (TB/s at 1, 2, 4 and 8: 5.0, 4.9, 4.0, 3.2 against 6 on the
+// tensor cores), but it has nothing to set up (1024 x 4096: 2.7 us at one
+// token and 3.8 at eight, against 4.6; 14336 x 4096 at one: 13.7 against 12.5).
+double estimate_dot_us(long long T, long long d_out, long long d_in) {
+  const double tbs = T == 1 ? 5.0 : T == 2 ? 4.9 : T <= 4 ? 4.0 : 3.2;
+  return 2.1 + static_cast<double>(d_out) * d_in / 1e6 / tbs;
 }
 
 // The ring of k-block stages in `room` bytes of shared memory, and the partials
@@ -2215,9 +2315,7 @@ dora_status_t launch_tile_i8(const LinearPlan& p, const LinearArgs& A, const int
   P.tmem_cols = 32;
   while (P.tmem_cols < static_cast<uint32_t>(p.n)) P.tmem_cols *= 2;
   P.idesc = idesc_i8_s32(kI8M, p.n);
-  // Two CTAs per SM where there are more CTAs than SMs, else one.
-  const long long ctas = static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits;
-  const size_t dyn = ctas > sms ? (size_t(113) << 10) - sizeof(TileI8Tail) : kTileI8MaxDynSmem;
+  const size_t dyn = tile_i8_shares_sm(p, sms) ? (size_t(113) << 10) - sizeof(TileI8Tail) : kTileI8MaxDynSmem;
   const I8Ring r = plan_i8_ring(dyn - 1024, kI8WBytes + static_cast<size_t>(p.n) * kI8K, p);
   P.stages = r.stages;
   P.part_off = r.part_off;
@@ -2279,35 +2377,40 @@ dora_status_t launch_pair_i8(const LinearPlan& p, const LinearArgs& A, const int
 }
 
 template <typename O>
-dora_status_t launch_tensor_i8(const LinearArgs& A, const int8_t* xq, const int8_t* wq, int ld,
-                               int sms, cudaStream_t cs) {
-  const LinearPlan p = plan_linear(A.T, A.d_out, A.d_in, sms);
-  return p.pair ? launch_pair_i8<O>(p, A, xq, wq, ld, sms, cs)
-                : launch_tile_i8<O>(p, A, xq, wq, ld, sms, cs);
-}
-
-template <typename O>
-dora_status_t launch_linear(const LinearArgs& A, void* ws, int sms, cudaStream_t cs) {
+dora_status_t launch_linear(const LinearArgs& A, void* ws, const DeviceInfo& d, cudaStream_t cs) {
   const bool vec = A.d_in % 16 == 0 && aligned16(A.xq) && aligned16(A.wq);
   const bool pads = linear_pads(A.T, A.d_in);
-  // Few tokens; or rows of whole 16-byte steps that start off a boundary,
-  // which TMA cannot read and the workspace (sized from the shape) does not
-  // cover.
-  if (A.T <= kDotMaxT || (!vec && !pads)) {
-    launch_dot_any<O>(A, vec, sms, cs);
+  double us = 0.0;
+  LinearPlan p{};
+  if (vec || pads) p = plan_linear(A.T, A.d_out, A.d_in, d, &us);
+  // Dot products: few tokens, where they are faster or rows are not of whole
+  // 16-byte steps; any number where rows are, but start off a boundary (TMA
+  // cannot read those, and the workspace, sized from the shape, has no room
+  // for copies).
+  const bool few = A.T <= kDotMaxT &&
+                   (!vec || estimate_dot_us(A.T, A.d_out, A.d_in) < us);
+  if (few || (!vec && !pads)) {
+    launch_dot_any<O>(A, vec, d.sms, cs);
     return launch_status();
   }
-  if (!pads) return launch_tensor_i8<O>(A, A.xq, A.wq, A.d_in, sms, cs);
-  const int ld = padded_k(A.d_in);
-  int8_t* xp = static_cast<int8_t*>(ws);
-  int8_t* wp = xp + linear_pad_x(A.T, A.d_in);
-  const PadArgs px{A.xq, xp, A.T, A.d_in, ld}, pw{A.wq, wp, A.d_out, A.d_in, ld};
-  const long long chunks = static_cast<long long>(std::max(A.T, A.d_out)) * (ld / 16);
-  const unsigned gx = static_cast<unsigned>(
-      std::min<long long>(ceil_div_ll(chunks, kPadThreads), 8ll * sms));
-  launch_stream(pad_rows_kernel, dim3(gx, 2), dim3(kPadThreads), 0, cs, px, pw);
-  const dora_status_t st = launch_status();
-  return st != DORA_OK ? st : launch_tensor_i8<O>(A, xp, wp, ld, sms, cs);
+  const int8_t *xq = A.xq, *wq = A.wq;
+  int ld = A.d_in;
+  if (pads) {
+    ld = padded_k(A.d_in);
+    int8_t* xp = static_cast<int8_t*>(ws);
+    int8_t* wp = xp + linear_pad_x(A.T, A.d_in);
+    const PadArgs px{A.xq, xp, A.T, A.d_in, ld}, pw{A.wq, wp, A.d_out, A.d_in, ld};
+    const long long chunks = static_cast<long long>(std::max(A.T, A.d_out)) * (ld / 16);
+    const unsigned gx = static_cast<unsigned>(
+        std::min<long long>(ceil_div_ll(chunks, kPadThreads), 8ll * d.sms));
+    launch_stream(pad_rows_kernel, dim3(gx, 2), dim3(kPadThreads), 0, cs, px, pw);
+    const dora_status_t st = launch_status();
+    if (st != DORA_OK) return st;
+    xq = xp;
+    wq = wp;
+  }
+  return p.pair ? launch_pair_i8<O>(p, A, xq, wq, ld, d.sms, cs)
+                : launch_tile_i8<O>(p, A, xq, wq, ld, d.sms, cs);
 }
 }  // namespace
 }  // namespace dora
@@ -2415,8 +2518,8 @@ dora_status_t dora_linear_i8(const int8_t* xq, const float* x_scale, const int8_
                static_cast<int>(d_in)};
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   TimedLaunch tl(cs);
-  return dt_out == DORA_BF16 ? launch_linear<__nv_bfloat16>(P, ws, di->sms, cs)
-                             : launch_linear<float>(P, ws, di->sms, cs);
+  return dt_out == DORA_BF16 ? launch_linear<__nv_bfloat16>(P, ws, *di, cs)
+                             : launch_linear<float>(P, ws, *di, cs);
 }
 
 }  // extern "C"
