@@ -2198,44 +2198,52 @@ bool tile_i8_shares_sm(const LinearPlan& p, int sms) {
          ceil_div_ll(p.kb, p.splits) <= kTileI8ShortK;
 }
 
-// Estimated time of a plan in us.  What bounds a k-block is the bytes an SM
-// takes in (or their HBM or L2 stream over all CTAs), the MMAs, or the turn of
-// the loop; every plan pays its set-up, the epilogue of its columns and, with a
-// split k, the exchange of partials.  The constants are a fit to the measured
-// times of all plans on 9 weights from 512 x 512 to 25600 x 5120 at 3 to 2048
-// tokens (1000 plans); the plan it picks is on average 1.2 % slower than the
-// fastest of them, where the fixed rule it replaced (pairs above 64 tokens with
-// the widest tile) was 20 % slower.
+// Estimated time of a plan in us; negative where a split k would not have all
+// its clusters resident at once (a second wave costs more than a split gains).
+// What bounds a wave is, per k-block, the bytes an SM takes in, the MMAs or the
+// turn of the loop, or the wave's share of the HBM or L2 stream; every plan
+// pays its set-up, the epilogue of its columns and, with a split k, the
+// exchange of partials.  The constants are a fit to the measured times of all
+// plans on 12 weights from 512 x 512 to 25600 x 5120 at 4 to 1500 tokens (2600
+// plans); the plan it picks is on average 1 to 2 % slower than the fastest,
+// where a fixed rule (pairs above 64 tokens with the widest tile) was 20 %
+// slower.
 double estimate_linear_us(const LinearPlan& p, long long T, long long d_out, long long d_in,
                           const DeviceInfo& d) {
   const double n = p.n, S = p.splits;
-  const double tiles = static_cast<double>(p.tiles_m) * p.tiles_n;
+  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
   const double kbs = static_cast<double>(ceil_div_ll(p.kb, p.splits));
   const double stage_kb = (kI8WBytes + (p.pair ? p.n / 2 : p.n) * kI8K) / 1000.0;
-  const double moved = static_cast<double>(d_out + T) * d_in / 1e6;  // MB from HBM
-  const double exchange = p.splits > 1 ? 0.33 + 0.041 * n * (S - 1) / S : 0.0;
+  const double exchange = p.splits > 1 ? 0.14 + 0.04 * n * (S - 1) / S : 0.0;
   const int cluster = (p.pair ? 2 : 1) * p.splits;
-  double slots = cluster == 8   ? d.clusters8
-                 : cluster == 4 ? d.clusters4
-                                : static_cast<double>(d.sms / cluster);
+  long long slots = cluster == 8   ? d.clusters8
+                    : cluster == 4 ? d.clusters4
+                                   : std::max(1, d.sms / cluster);
   double base, kblock, epilogue;
   if (p.pair) {
-    base = 4.1;
-    kblock = std::max({stage_kb / 147.0, 0.00081 * n, 0.072});
-    epilogue = 0.008 * n / S;
+    base = 5.15;
+    kblock = std::max({stage_kb / 162.0, 0.00107 * n, 0.099});
+    epilogue = 0.0053 * n / S;
   } else {
-    const bool two = tiles * S > d.sms;
-    if (two) slots *= 2;
-    const int on_sm = std::min(tiles, slots) * S > d.sms ? 2 : 1;
-    base = 2.35;
-    kblock = std::max({on_sm * stage_kb / (on_sm == 2 ? 98.0 : 147.0), on_sm * 0.00125 * n, 0.18});
-    epilogue = 0.21 + 0.010 * n / S;
+    base = 2.02;
+    if (tiles * p.splits > d.sms) slots *= 2;
+    const bool two = std::min(tiles, slots) * p.splits > d.sms;  // CTAs on an SM
+    kblock = two ? std::max({stage_kb / 52.0, 0.0035 * n, 0.223})
+                 : std::max({stage_kb / 162.0, 0.00174 * n, 0.223});
+    epilogue = 0.355 + 0.0066 * n / S;
   }
-  const double waves = std::ceil(tiles / slots);
-  const double main = p.pair ? waves * kbs * kblock + epilogue + exchange
-                             : waves * (kbs * kblock + epilogue + exchange);
-  const double l2 = tiles * (p.pair ? 2 : 1) * p.kb * stage_kb / 1000.0;
-  return base + std::max(main, 0.63 + std::max(moved / 6.0, l2 / 17.7));
+  const long long full = tiles / slots, rest = tiles % slots;
+  if (p.splits > 1 && full + (rest > 0) > 1) return -1.0;
+  const double moved = static_cast<double>(d_out + T) * d_in / 1e6;  // MB from HBM
+  const double l2 = tiles * (p.pair ? 2.0 : 1.0) * p.kb * stage_kb / 1000.0;
+  const double stream = std::max(moved / 6.63, l2 / 27.5) / tiles;  // us per tile
+  const double wave = std::max(kbs * kblock, 0.44 + stream * slots);
+  const double last = rest > 0 ? std::max(kbs * kblock, 0.44 + stream * rest) : 0.0;
+  // (two CTAs on an SM, or the two accumulators of a pair, hide most of the
+  // epilogues but the last)
+  const double waves = static_cast<double>(full + (rest > 0));
+  const double shown = p.pair ? 1.0 : waves > 1 ? 0.6 * waves : 1.0;
+  return base + full * wave + last + shown * epilogue + exchange;
 }
 
 // The fastest plan by that estimate: a tile of up to 64, 128, 192 or 256
@@ -2259,7 +2267,7 @@ LinearPlan plan_linear(int T, int d_out, int d_in, const DeviceInfo& d, double* 
         p.n = round_up_int(static_cast<int>(ceil_div_ll(T, p.tiles_n)),
                            pair || p.splits == 8 ? 32 : 16);
         const double t = estimate_linear_us(p, T, d_out, d_in, d);
-        if (best.n == 0 || t < *us) {
+        if (t >= 0.0 && (best.n == 0 || t < *us)) {
           best = p;
           *us = t;
         }
@@ -2269,7 +2277,7 @@ LinearPlan plan_linear(int T, int d_out, int d_in, const DeviceInfo& d, double* 
 }
 
 // Estimated time of the dot-product kernel: its stream of the weight slows
-// with the tokens (TB/s at 1, 2, 4 and 8: 5.0, 4.9, 4.0, 3.2 against 6 on the
+// with the tokens (TB/s at 1, 2, 4 and 8: 5.0, 4.9, 4.0, 3.2 against 6.6 on the
 // tensor cores), but it has nothing to set up (1024 x 4096: 2.7 us at one
 // token and 3.8 at eight, against 4.6; 14336 x 4096 at one: 13.7 against 12.5).
 double estimate_dot_us(long long T, long long d_out, long long d_in) {
@@ -2278,8 +2286,10 @@ double estimate_dot_us(long long T, long long d_out, long long d_in) {
 }
 
 // The ring of k-block stages in `room` bytes of shared memory, and the partials
-// of a split k: behind a ring of at least four stages (or all k-blocks), else
+// of a split k: behind a ring of at least six stages (or all k-blocks), else
 // over the ring, at the price of a cluster barrier before they are written.
+// (Behind a ring of four 32 KiB stages a k-block took 0.42 us, not 0.26.)
+constexpr size_t kI8MinStages = 6;
 struct I8Ring {
   int stages;
   uint32_t part_off;
@@ -2294,7 +2304,7 @@ I8Ring plan_i8_ring(size_t room, size_t stage, const LinearPlan& p) {
                           ? size_t(kI8MaxStages)
                           : std::min<size_t>(kI8MaxStages, ceil_div_ll(p.kb, p.splits));
   I8Ring r;
-  r.part_over_ring = part + std::min<size_t>(most, 4) * stage > room;
+  r.part_over_ring = part + std::min(most, kI8MinStages) * stage > room;
   r.stages = static_cast<int>(std::min(most, (room - (r.part_over_ring ? 0 : part)) / stage));
   const size_t ring = r.stages * stage;
   r.part_off = r.part_over_ring ? 0 : static_cast<uint32_t>(ring);
