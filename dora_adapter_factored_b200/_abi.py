@@ -603,16 +603,19 @@ def dora_norm_finalize(sq: torch.Tensor, m: Optional[torch.Tensor] = None, eps: 
 
 # ------------------------------------------------- 8-bit serving of a merged weight
 #
-# These calls run once per layer and decoding step, so their marshalling is
-# kept short: one check per operand that the caller passed, none for what is
-# allocated here, and the current stream's handle without a Stream object.
+# These calls run once per layer and decoding step, often on microseconds of
+# GPU work, so their marshalling is kept short: one check per operand that the
+# caller passed, none for what is allocated here, and the current stream's
+# handle without a Stream object.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_I8, _F32 = torch.int8, torch.float32
 
 
 def _here(t: torch.Tensor, name: str) -> int:
-    """Index of the device of a call's first operand, which must be the current
-    one (the library launches there); the others are checked against it."""
+    """Index of the device of a call's first operand, a matrix, which must be on
+    the current device (the library launches there); the others are checked
+    against it."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     index = t.get_device()
@@ -621,14 +624,19 @@ def _here(t: torch.Tensor, name: str) -> int:
     if index != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device} but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions (got shape {tuple(t.shape)})")
     return index
 
 
 def _arg(t: torch.Tensor, name: str, dtype, shape, index: int) -> int:
     """Data pointer of an operand: dtype, shape, contiguity and device checked."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
-            and t.get_device() == index and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(t, torch.Tensor) and t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
     _dev(t, name, dtype, shape)
@@ -642,32 +650,38 @@ def _current(stream, index: int) -> int:
     return _stream(stream)
 
 
-def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
-    """An output or workspace, allocated for the stream that the call runs on."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+def _on_stream(stream, like: torch.Tensor):
+    """Context in which what a call allocates belongs to the stream it runs on."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) \
             else torch.cuda.default_stream(like.device)
-    with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+    return torch.cuda.stream(stream)
 
 
-def _matrix(t: torch.Tensor, name: str):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions (got shape {tuple(t.shape)})")
-    return t.shape
+def _out_matrix(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dtype, index: int,
+                stream):
+    """An output of `like`'s shape, the caller's or a new one: (tensor, pointer)."""
+    if t is not None:
+        return t, _arg(t, name, dtype, like.shape, index)
+    if stream is None:
+        t = torch.empty_like(like, dtype=dtype)
+    else:
+        with _on_stream(stream, like):
+            t = torch.empty_like(like, dtype=dtype)
+    return t, t.data_ptr()
 
 
-def _out(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dtype, index: int,
-         stream):
-    """An output the caller passed, or a new one: (tensor, its pointer)."""
-    if t is None:
-        t = _new(like, shape, dtype, stream)
-        return t, t.data_ptr()
-    return t, _arg(t, name, dtype, shape, index)
+def _out_vector(t: Optional[torch.Tensor], name: str, like: torch.Tensor, n: int, dtype,
+                index: int, stream):
+    """As _out_matrix, [n]."""
+    if t is not None:
+        return t, _arg(t, name, dtype, (n,), index)
+    if stream is None:
+        t = like.new_empty(n, dtype=dtype)
+    else:
+        with _on_stream(stream, like):
+            t = like.new_empty(n, dtype=dtype)
+    return t, t.data_ptr()
 
 
 def dora_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -677,11 +691,13 @@ def dora_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     lib = _lib or load_library()
     index = _here(x, "x")
     dt = _dtype_code(x)
-    shape = rows, cols = _matrix(x, "x")
-    q, pq = _out(q, "q", x, shape, torch.int8, index, stream)
-    scale, ps = _out(scale, "scale", x, (rows,), torch.float32, index, stream)
-    _check(lib.dora_quantize_rows(_arg(x, "x", x.dtype, shape, index), dt, rows, cols, pq, ps,
-                                  _current(stream, index)), "dora_quantize_rows")
+    rows, cols = shape = x.shape
+    px = _arg(x, "x", x.dtype, shape, index)
+    q, pq = _out_matrix(q, "q", x, _I8, index, stream)
+    scale, ps = _out_vector(scale, "scale", x, rows, _F32, index, stream)
+    status = lib.dora_quantize_rows(px, dt, rows, cols, pq, ps, _current(stream, index))
+    if status:
+        raise DoraError(status, "dora_quantize_rows")
     return q, scale
 
 
@@ -692,15 +708,17 @@ def dora_dequantize_rows(q: torch.Tensor, scale: torch.Tensor,
     or fp32; x's own where x is given)."""
     lib = _lib or load_library()
     index = _here(q, "q")
-    shape = rows, cols = _matrix(q, "q")
-    dtype = x.dtype if isinstance(x, torch.Tensor) else dtype
+    rows, cols = shape = q.shape
+    if x is not None:
+        dtype = x.dtype
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}: the library takes float32 or bfloat16")
-    pq = _arg(q, "q", torch.int8, shape, index)
-    ps = _arg(scale, "scale", torch.float32, (rows,), index)
-    x, px = _out(x, "x", q, shape, dtype, index, stream)
-    _check(lib.dora_dequantize_rows(pq, ps, _DT[dtype], rows, cols, px, _current(stream, index)),
-           "dora_dequantize_rows")
+    pq = _arg(q, "q", _I8, shape, index)
+    ps = _arg(scale, "scale", _F32, (rows,), index)
+    x, px = _out_matrix(x, "x", q, dtype, index, stream)
+    status = lib.dora_dequantize_rows(pq, ps, _DT[dtype], rows, cols, px, _current(stream, index))
+    if status:
+        raise DoraError(status, "dora_dequantize_rows")
     return x
 
 
@@ -714,21 +732,21 @@ def dora_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float,
     lib = _lib or load_library()
     index = _here(x, "x")
     dt = _dtype_code(x)
-    shape = T, d = _matrix(x, "x")
+    T, d = shape = x.shape
     dtype = x.dtype
     px = _arg(x, "x", dtype, shape, index)
     pw = _arg(weight, "weight", dtype, (d,), index)
+    pr = ph = None
     if residual is not None:
         pr = _arg(residual, "residual", dtype, shape, index)
-        h_out, ph = _out(h_out, "h_out", x, shape, dtype, index, stream)
-    elif h_out is None:
-        pr = ph = None
-    else:
+        h_out, ph = _out_matrix(h_out, "h_out", x, dtype, index, stream)
+    elif h_out is not None:
         raise ValueError("h_out is the sum with a residual: pass residual too")
-    q, pq = _out(q, "q", x, shape, torch.int8, index, stream)
-    scale, ps = _out(scale, "scale", x, (T,), torch.float32, index, stream)
-    _check(lib.dora_rmsnorm_quant(px, pr, pw, float(eps), dt, T, d, ph, pq, ps,
-                                  _current(stream, index)), "dora_rmsnorm_quant")
+    q, pq = _out_matrix(q, "q", x, _I8, index, stream)
+    scale, ps = _out_vector(scale, "scale", x, T, _F32, index, stream)
+    status = lib.dora_rmsnorm_quant(px, pr, pw, eps, dt, T, d, ph, pq, ps, _current(stream, index))
+    if status:
+        raise DoraError(status, "dora_rmsnorm_quant")
     return q, scale, h_out
 
 
@@ -745,26 +763,37 @@ def dora_linear_i8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor,
     int8; scales and bias fp32."""
     lib = _lib or load_library()
     index = _here(xq, "xq")
-    T, d_in = _matrix(xq, "xq")
-    d_out = _matrix(wq, "wq")[0]
-    px = _arg(xq, "xq", torch.int8, (T, d_in), index)
-    psx = _arg(x_scale, "x_scale", torch.float32, (T,), index)
-    pw = _arg(wq, "wq", torch.int8, (d_out, d_in), index)
-    psw = _arg(w_scale, "w_scale", torch.float32, (d_out,), index)
-    pb = None if bias is None else _arg(bias, "bias", torch.float32, (d_out,), index)
-    dtype = y.dtype if isinstance(y, torch.Tensor) else dtype
+    _here(wq, "wq")
+    T, d_in = shape = xq.shape
+    d_out = wq.shape[0]
+    px = _arg(xq, "xq", _I8, shape, index)
+    psx = _arg(x_scale, "x_scale", _F32, (T,), index)
+    pw = _arg(wq, "wq", _I8, (d_out, d_in), index)
+    psw = _arg(w_scale, "w_scale", _F32, (d_out,), index)
+    pb = None if bias is None else _arg(bias, "bias", _F32, (d_out,), index)
+    if y is not None:
+        dtype = y.dtype
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}: the library takes float32 or bfloat16")
-    y, py = _out(y, "y", xq, (T, d_out), dtype, index, stream)
+    if y is not None:
+        py = _arg(y, "y", dtype, (T, d_out), index)
+    else:
+        if stream is None:
+            y = xq.new_empty((T, d_out), dtype=dtype)
+        else:
+            with _on_stream(stream, xq):
+                y = xq.new_empty((T, d_out), dtype=dtype)
+        py = y.data_ptr()
     pws, nws = None, 0
-    if ws is None and d_in % 16:  # rows of whole 16-byte steps need no workspace
-        nws = lib.dora_linear_i8_workspace_size(T, d_out, d_in)
-        if nws:
-            ws = _new(xq, (nws,), torch.uint8, stream)
-            pws = ws.data_ptr()
-    elif ws is not None:
+    if ws is not None:
         pws = _arg(ws, "ws", ws.dtype, ws.shape, index)
         nws = ws.numel() * ws.element_size()
-    _check(lib.dora_linear_i8(px, psx, pw, psw, pb, _DT[dtype], T, d_out, d_in, py, pws, nws,
-                              _current(stream, index)), "dora_linear_i8")
+    elif d_in % 16:  # rows of whole 16-byte steps need no workspace
+        nws = lib.dora_linear_i8_workspace_size(T, d_out, d_in)
+        if nws:
+            ws, pws = _out_vector(None, "ws", xq, nws, torch.uint8, index, stream)
+    status = lib.dora_linear_i8(px, psx, pw, psw, pb, _DT[dtype], T, d_out, d_in, py, pws, nws,
+                                _current(stream, index))
+    if status:
+        raise DoraError(status, "dora_linear_i8")
     return y
