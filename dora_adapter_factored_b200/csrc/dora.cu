@@ -2020,43 +2020,56 @@ constexpr int64_t kMaxQuantRows = int64_t(1) << 30;
 constexpr int64_t kMaxQuantCols = int64_t(1) << 30;
 constexpr int64_t kMaxLinearTokens = int64_t(1) << 23;  // token tiles are a grid's second axis
 
-// Blocks the row kernels keep per SM before they walk rows.
-constexpr int kRowThreadsPerSm = 1024;
-
-template <typename E, int VEC, int MODE>
-void launch_rows(const RowArgs& P, int sms, cudaStream_t cs) {
-  const long long nvec = P.d / VEC;
-  const long long want = ceil_div_ll(ceil_div_ll(nvec, row_nv(VEC)), 32) * 32;
-  const bool fits = want <= kRowThreads;
-  const int threads = static_cast<int>(std::min<long long>(want, kRowThreads));
+template <typename E, int VEC, int NV, int MODE, bool RAGGED>
+void launch_rows_nv(const RowArgs& P, long long nvec, int sms, cudaStream_t cs) {
+  const long long want = ceil_div_ll(ceil_div_ll(nvec, NV), 32) * 32;
+  const bool fits = want <= row_max_threads(MODE);
+  const int threads = fits ? static_cast<int>(want) : kRowThreads;
   const int by = fits && threads == 32 ? 8 : 1;  // one-warp rows share a block
   const long long groups = ceil_div_ll(P.rows, by);
-  const int per_sm = std::max(1, kRowThreadsPerSm / (threads * by));
-  const unsigned grid =
-      static_cast<unsigned>(std::min<long long>(groups, static_cast<long long>(sms) * per_sm));
+  const int per_sm = std::max(1, (fits ? row_threads_per_sm(MODE, NV) : 2 * kRowThreads) /
+                                     (threads * by));
+  long long grid = static_cast<long long>(sms) * per_sm;
+  if (RAGGED && grid * by % VEC != 0) grid = std::max<long long>(VEC, grid / VEC * VEC);
+  const dim3 blocks(static_cast<unsigned>(std::min(groups, grid)));
   if (fits)
-    launch_stream(row_quant_kernel<E, VEC, MODE>, dim3(grid), dim3(threads, by), 0, cs, P);
+    launch_stream(row_quant_kernel<E, VEC, NV, MODE, RAGGED>, blocks, dim3(threads, by), 0, cs, P);
   else
-    launch_stream(row_quant_long_kernel<E, VEC, MODE>, dim3(grid), dim3(threads), 0, cs, P);
+    launch_stream(row_quant_long_kernel<E, VEC, MODE, RAGGED>, blocks, dim3(threads), 0, cs, P);
+}
+
+template <typename E, int VEC, int MODE, bool RAGGED>
+void launch_rows(const RowArgs& P, int sms, cudaStream_t cs) {
+  // The most vectors a row can touch.
+  const long long nvec = ceil_div_ll(static_cast<long long>(P.d) + (RAGGED ? VEC - 1 : 0), VEC);
+  if constexpr (VEC == 1)
+    launch_rows_nv<E, VEC, kRowScalars, MODE, RAGGED>(P, nvec, sms, cs);
+  else if (nvec <= 32)
+    launch_rows_nv<E, VEC, 1, MODE, RAGGED>(P, nvec, sms, cs);
+  else
+    launch_rows_nv<E, VEC, kRowVecs, MODE, RAGGED>(P, nvec, sms, cs);
+}
+
+// Vectors where the matrices are aligned as a whole (ragged where a row is not
+// a whole number of them), elements otherwise.
+template <typename E, int VEC, int MODE>
+void launch_rows_vec(const RowArgs& P, int sms, cudaStream_t cs) {
+  const bool vec = aligned16(P.x) && aligned16(P.residual) && aligned16(P.h_out) &&
+                   (reinterpret_cast<uintptr_t>(P.q) & (VEC - 1)) == 0;
+  if (vec && P.d % VEC == 0 && aligned16(P.weight))
+    launch_rows<E, VEC, MODE, false>(P, sms, cs);
+  else if (vec && aligned16(P.weight))
+    launch_rows<E, VEC, MODE, true>(P, sms, cs);
+  else
+    launch_rows<E, 1, MODE, false>(P, sms, cs);
 }
 
 template <int MODE>
 void launch_rows_dt(const RowArgs& P, dora_dtype_t dt, int sms, cudaStream_t cs) {
-  const int v = dt == DORA_BF16 ? 8 : 4;
-  const bool vec = P.d % v == 0 && aligned16(P.x) && aligned16(P.residual) &&
-                   aligned16(P.weight) && aligned16(P.h_out) &&
-                   (reinterpret_cast<uintptr_t>(P.q) & (v - 1)) == 0;
-  if (dt == DORA_BF16) {
-    if (vec)
-      launch_rows<__nv_bfloat16, 8, MODE>(P, sms, cs);
-    else
-      launch_rows<__nv_bfloat16, 1, MODE>(P, sms, cs);
-  } else {
-    if (vec)
-      launch_rows<float, 4, MODE>(P, sms, cs);
-    else
-      launch_rows<float, 1, MODE>(P, sms, cs);
-  }
+  if (dt == DORA_BF16)
+    launch_rows_vec<__nv_bfloat16, 8, MODE>(P, sms, cs);
+  else
+    launch_rows_vec<float, 4, MODE>(P, sms, cs);
 }
 
 // Element alignment of a pointer that may be NULL.
@@ -2095,13 +2108,29 @@ dora_status_t run_rows(const RowArgs& P, dora_dtype_t dt, int mode, dora_stream_
 }
 
 template <typename E, int VEC>
-void launch_dequant(const int8_t* q, const float* scale, int64_t rows, int cols, void* x,
+void launch_dequant(const int8_t* q, const float* scale, int64_t rows, int cols, E* x,
                     cudaStream_t cs) {
   const StreamGrid g = stream_grid(rows, static_cast<int>(ceil_div_ll(cols, VEC)),
                                    kDequantRowUnroll, 4 * kStreamSlots);
   launch_stream(dequant_rows_kernel<E, VEC>, dim3(g.gx, std::min(g.gy, 65535)),
-                dim3(kStreamThreads), 0, cs, q, scale, static_cast<long long>(rows), cols,
-                static_cast<E*>(x), g.bx);
+                dim3(kStreamThreads), 0, cs, q, scale, static_cast<long long>(rows), cols, x,
+                g.bx);
+}
+
+template <typename E, int VEC>
+void launch_dequant_vec(const int8_t* q, const float* scale, int64_t rows, int64_t cols, void* x,
+                        cudaStream_t cs) {
+  E* out = static_cast<E*>(x);
+  const int c = static_cast<int>(cols);
+  if (!aligned16(x) || (reinterpret_cast<uintptr_t>(q) & (VEC - 1)) != 0)
+    return launch_dequant<E, 1>(q, scale, rows, c, out, cs);
+  if (cols % VEC == 0) return launch_dequant<E, VEC>(q, scale, rows, c, out, cs);
+  const long long vecs = ceil_div_ll(static_cast<long long>(rows) * cols, VEC);
+  const unsigned grid =
+      static_cast<unsigned>(std::min<long long>(ceil_div_ll(vecs, kStreamThreads),
+                                                4ll * kStreamSlots));
+  launch_stream(dequant_flat_kernel<E, VEC>, dim3(grid), dim3(kStreamThreads), 0, cs, q, scale,
+                static_cast<long long>(rows), c, out);
 }
 
 // ---- linear layer
@@ -2451,21 +2480,12 @@ dora_status_t dora_dequantize_rows(const int8_t* q, const float* scale, dora_dty
   if (di == nullptr) return DORA_ERR_CUDA;
   if (!di->supported) return DORA_ERR_UNSUPPORTED;
   if (rows == 0) return DORA_OK;
-  const int v = dt == DORA_BF16 ? 8 : 4, c = static_cast<int>(cols);
-  const bool vec = cols % v == 0 && aligned16(x) && aligned_to(q, v);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   TimedLaunch tl(cs);
-  if (dt == DORA_BF16) {
-    if (vec)
-      launch_dequant<__nv_bfloat16, 8>(q, scale, rows, c, x, cs);
-    else
-      launch_dequant<__nv_bfloat16, 1>(q, scale, rows, c, x, cs);
-  } else {
-    if (vec)
-      launch_dequant<float, 4>(q, scale, rows, c, x, cs);
-    else
-      launch_dequant<float, 1>(q, scale, rows, c, x, cs);
-  }
+  if (dt == DORA_BF16)
+    launch_dequant_vec<__nv_bfloat16, 8>(q, scale, rows, cols, x, cs);
+  else
+    launch_dequant_vec<float, 4>(q, scale, rows, cols, x, cs);
   return launch_status();
 }
 

@@ -100,23 +100,158 @@ struct RowVec<float, 1> {
   static __device__ __forceinline__ raw pack(const float (&v)[1]) { return v[0]; }
 };
 
+// Vectors are taken at multiples of VEC elements of the whole matrix, so that
+// x, the residual, h and the codes share one alignment whatever the row length:
+// a row then starts `lead` elements into its first vector, and its first and
+// last vectors may hold elements of the neighbouring rows.  Those are loaded
+// too and masked out (as bits: they may be anything, and may be written
+// meanwhile where h goes over x); only the row's own elements [lo, hi) are
+// stored, one by one.  A vector that reaches past the matrix is loaded
+// element by element.
+template <typename E, int VEC>
+__device__ __forceinline__ typename RowVec<E, VEC>::raw load_part(const E* p, int lo, int hi) {
+  float v[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) v[e] = e >= lo && e < hi ? static_cast<float>(p[e]) : 0.f;
+  return RowVec<E, VEC>::pack(v);  // exact: the values are E's
+}
+
+template <typename E, int VEC>
+__device__ __forceinline__ typename RowVec<E, VEC>::raw mask_part(
+    const typename RowVec<E, VEC>::raw& r, int lo, int hi) {
+  static_assert(sizeof(r) == 16, "vectors of four words");
+  uint4 w = *reinterpret_cast<const uint4*>(&r);
+  uint32_t* p = reinterpret_cast<uint32_t*>(&w);
+  constexpr int kPerWord = VEC / 4;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t keep = 0;
+#pragma unroll
+    for (int j = 0; j < kPerWord; ++j) {
+      const int e = k * kPerWord + j;
+      if (e >= lo && e < hi) keep |= kPerWord == 1 ? 0xffffffffu : 0xffffu << (16 * j);
+    }
+    p[k] &= keep;
+  }
+  return *reinterpret_cast<const typename RowVec<E, VEC>::raw*>(&w);
+}
+
+template <typename E, int VEC>
+__device__ __forceinline__ void store_part(E* p, const typename RowVec<E, VEC>::raw& r, int lo,
+                                           int hi) {
+  float v[VEC];
+  RowVec<E, VEC>::unpack(r, v);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e)
+    if (e >= lo && e < hi) p[e] = static_cast<E>(v[e]);
+}
+
 // The codes of VEC values: rint(u inv), half to even.  |u inv| <= 127 up to
 // two roundings, so the nearest integer is at most 127.
 template <int VEC>
-__device__ __forceinline__ void store_codes(int8_t* p, const float (&u)[VEC], float inv) {
+__device__ __forceinline__ void store_codes(int8_t* p, const float (&u)[VEC], float inv, int lo,
+                                            int hi) {
   uint32_t w[(VEC + 3) / 4];
 #pragma unroll
   for (int i = 0; i < (VEC + 3) / 4; ++i) w[i] = 0;
 #pragma unroll
   for (int e = 0; e < VEC; ++e)
     w[e / 4] |= (static_cast<uint32_t>(__float2int_rn(u[e] * inv)) & 0xffu) << (8 * (e % 4));
-  if constexpr (VEC == 8)
+  if (lo > 0 || hi < VEC) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (e >= lo && e < hi) p[e] = static_cast<int8_t>(w[e / 4] >> (8 * (e % 4)));
+  } else if constexpr (VEC == 8) {
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  else if constexpr (VEC == 4)
+  } else if constexpr (VEC == 4) {
     *reinterpret_cast<uint32_t*>(p) = w[0];
-  else
+  } else {
     *p = static_cast<int8_t>(w[0]);
+  }
 }
+
+// Elements [VEC - n, 2 VEC - n) of the two vectors a, b, n in 0 .. VEC - 1:
+// shifts by one, two and four elements under the bits of n.
+template <typename E, int VEC>
+__device__ __forceinline__ typename RowVec<E, VEC>::raw shift_in(
+    const typename RowVec<E, VEC>::raw& a, const typename RowVec<E, VEC>::raw& b, int n) {
+  static_assert(sizeof(a) == 16, "vectors of four words");
+  uint32_t w[8];
+  *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(&a);
+  *reinterpret_cast<uint4*>(w + 4) = *reinterpret_cast<const uint4*>(&b);
+  if constexpr (VEC == 8) {
+#pragma unroll
+    for (int i = 7; i >= 1; --i) w[i] = n & 1 ? __funnelshift_l(w[i - 1], w[i], 16) : w[i];
+    n >>= 1;
+  }
+#pragma unroll
+  for (int i = 7; i >= 2; --i) w[i] = n & 1 ? w[i - 1] : w[i];
+#pragma unroll
+  for (int i = 7; i >= 4; --i) w[i] = n & 2 ? w[i - 2] : w[i];
+  typename RowVec<E, VEC>::raw out;
+  *reinterpret_cast<uint4*>(&out) = *reinterpret_cast<const uint4*>(w + 4);
+  return out;
+}
+
+// A row in vectors: `vecs` of them from element `base` of the matrix, its own
+// elements from `lead`.  RAGGED false: rows are whole vectors.
+template <int VEC, bool RAGGED>
+struct RowSpan {
+  size_t base;
+  int lead, vecs, d;
+  __device__ __forceinline__ RowSpan(long long row, int cols) {
+    const size_t at = static_cast<size_t>(row) * cols;
+    lead = RAGGED ? static_cast<int>(at % VEC) : 0;
+    base = at - lead;
+    vecs = RAGGED ? (lead + cols + VEC - 1) / VEC : cols / VEC;
+    d = cols;
+  }
+  // The row's own elements [lo, hi) of its vector c.
+  __device__ __forceinline__ int lo(int c) const { return RAGGED && c == 0 ? lead : 0; }
+  __device__ __forceinline__ int hi(int c) const {
+    return RAGGED ? min(VEC, lead + d - c * VEC) : VEC;
+  }
+  // Vector c of a matrix of `total` elements; own() then masks it (apart, so
+  // that all of a row's loads are on their way before the first is used).
+  template <typename E>
+  __device__ __forceinline__ typename RowVec<E, VEC>::raw load(const void* m, int c,
+                                                               size_t total) const {
+    const size_t at = base + static_cast<size_t>(c) * VEC;
+    const E* p = static_cast<const E*>(m) + at;
+    if (RAGGED && at + VEC > total) return load_part<E, VEC>(p, 0, static_cast<int>(total - at));
+    return *reinterpret_cast<const typename RowVec<E, VEC>::raw*>(p);
+  }
+  template <typename E>
+  __device__ __forceinline__ void own(typename RowVec<E, VEC>::raw& v, int c) const {
+    if constexpr (RAGGED)
+      if (lo(c) > 0 || hi(c) < VEC) v = mask_part<E, VEC>(v, lo(c), hi(c));
+  }
+  template <typename E>
+  __device__ __forceinline__ void store(void* m, int c,
+                                        const typename RowVec<E, VEC>::raw& v) const {
+    E* p = static_cast<E*>(m) + base + static_cast<size_t>(c) * VEC;
+    if (RAGGED && (lo(c) > 0 || hi(c) < VEC))
+      store_part<E, VEC>(p, v, lo(c), hi(c));
+    else
+      *reinterpret_cast<typename RowVec<E, VEC>::raw*>(p) = v;
+  }
+  // The weight at the columns of vector c, zero outside the row: where rows are
+  // ragged, put together from two vectors of the weight (element by element,
+  // each load of a warp touched four times the lines: 27 against 17 us at
+  // [2047, 4099] fp32).
+  template <typename E>
+  __device__ __forceinline__ typename RowVec<E, VEC>::raw weight(const void* w, int c) const {
+    using RV = RowVec<E, VEC>;
+    const E* p = static_cast<const E*>(w);
+    auto whole = [&](int v) -> typename RV::raw {
+      if (v < 0 || v * VEC >= d) return RV::zero();
+      if (v * VEC + VEC > d) return load_part<E, VEC>(p + v * VEC, 0, d - v * VEC);
+      return *reinterpret_cast<const typename RV::raw*>(p + v * VEC);
+    };
+    if constexpr (RAGGED) return shift_in<E, VEC>(whole(c - 1), whole(c), lead);
+    return *reinterpret_cast<const typename RV::raw*>(p + c * VEC);
+  }
+};
 
 // h of one vector: x, or x + residual rounded to the dtype.
 template <typename E, int VEC, int MODE>
@@ -182,106 +317,135 @@ __device__ __forceinline__ void row_reduce(float& sq, uint32_t& top, int warps, 
   top = __reduce_max_sync(0xffffffffu, top);
 }
 
-// Factor of the codes and the row's scale from its sum of squares and
-// maximum.  A row that is not finite gets codes 0 and scale NaN; one whose
-// step would not be a normal number gets codes 0 and scale 0.
+// Factor of the codes from the row's maximum (and, where it is a norm, its sum
+// of squares, which has to be finite): 0 for a row that is not finite and for
+// one whose step max / 127 would not be a normal number.
 template <int MODE>
-__device__ __forceinline__ void row_scale(float sq, uint32_t top, int d, float eps, float& inv,
-                                          float& scale) {
-  const float a = __uint_as_float(top);
-  const float step = __fdiv_rn(a, kCodeMax);
-  float rstd = 1.f;
-  bool finite = top < kInfBits;
-  if constexpr (MODE != kRowQuant) {
-    finite = finite && __float_as_uint(sq) < kInfBits;
-    rstd = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sq, static_cast<float>(d)), eps)));
-  }
-  inv = 0.f;
-  scale = 0.f;
-  if (!finite) {
-    scale = __uint_as_float(0x7fc00000u);
-  } else if (step >= kMinNormal) {
-    inv = __fdiv_rn(kCodeMax, a);
-    scale = MODE == kRowQuant ? step : __fmul_rn(step, rstd);
-  }
+__device__ __forceinline__ float row_inv(float sq, uint32_t top) {
+  bool live = top < kInfBits && __uint_as_float(top) >= kCodeMax * kMinNormal;
+  if constexpr (MODE != kRowQuant) live = live && __float_as_uint(sq) < kInfBits;
+  return live ? __fdiv_rn(kCodeMax, __uint_as_float(top)) : 0.f;
 }
 
-// Rows of up to kRowNV vectors per thread.  A group of blockDim.x threads (a
-// multiple of 32) takes a row; blockDim.y groups share a block only where a
-// group is one warp.  Blocks walk the rows with the grid's stride.
-constexpr int kRowVecs = 4;     // 16-byte vectors per thread
-constexpr int kRowScalars = 16; // elements per thread where rows are not aligned
-constexpr int kRowThreads = 512;
-__host__ __device__ constexpr int row_nv(int vec) { return vec > 1 ? kRowVecs : kRowScalars; }
+// The row's scale, which no thread but the one that stores it waits for: NaN
+// for a row that is not finite, 0 where there is no step.
+template <int MODE>
+__device__ __forceinline__ float row_scale(float sq, uint32_t top, float inv, int d, float eps) {
+  const bool finite =
+      top < kInfBits && (MODE == kRowQuant || __float_as_uint(sq) < kInfBits);
+  if (!finite) return __uint_as_float(0x7fc00000u);
+  if (inv == 0.f) return 0.f;
+  const float step = __fdiv_rn(__uint_as_float(top), kCodeMax);
+  if constexpr (MODE == kRowQuant) return step;
+  const float mean = __fdiv_rn(sq, static_cast<float>(d));
+  return __fmul_rn(step, __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(mean, eps))));
+}
 
-template <typename E, int VEC, int MODE>
-__global__ void __launch_bounds__(kRowThreads) row_quant_kernel(const RowArgs P) {
+// Rows of up to NV vectors per thread.  A group of blockDim.x threads (a
+// multiple of 32) takes a row; blockDim.y groups share a block only where a
+// group is one warp.  Blocks walk the rows with the grid's stride, which has
+// to be the blocks that are resident at once (more would run as a second
+// wave: 103 instead of 71 us at [25600, 5120]); the register bound keeps the
+// two in step.
+// NV: 16-byte vectors per thread, 4, or 1 for rows that a warp holds so (short
+// rows need many of them in flight); or elements, where the matrix itself is
+// not aligned.
+constexpr int kRowVecs = 4;
+constexpr int kRowScalars = 16;
+constexpr int kRowThreads = 512;  // of a block that walks a row in two passes
+// Registers per thread, and the threads per SM they leave room for: 48 to 64
+// KiB of loads in flight (the norm with a residual has two streams, and the
+// weight, per thread).
+__host__ __device__ constexpr int row_regs(int mode, int nv) {
+  return nv == 1 ? 40 : mode == kRowQuant ? 64 : mode == kRowNorm ? 96 : 128;
+}
+__host__ __device__ constexpr int row_threads_per_sm(int mode, int nv) {
+  return 65536 / row_regs(mode, nv);
+}
+// The largest block that its registers allow, in whole 512 threads.
+__host__ __device__ constexpr int row_max_threads(int mode) {
+  return row_threads_per_sm(mode, kRowVecs) >= 1024 ? 1024 : 512;
+}
+
+template <typename E, int VEC, int NV, int MODE, bool RAGGED>
+__global__ void __maxnreg__(row_regs(MODE, NV)) row_quant_kernel(const RowArgs P) {
   using RV = RowVec<E, VEC>;
   using raw = typename RV::raw;
-  constexpr int NV = row_nv(VEC);
+  // The weight stays in registers over a block's rows: these start alike, since
+  // the grid's stride is a multiple of VEC rows where rows are ragged.
+  // Element by element there is no room for it, and it is read for each row.
+  constexpr bool kHoldWeight = MODE != kRowQuant && VEC > 1;
+  // The next row's loads are on their way while a row is reduced and stored:
+  // 93 instead of 88 % of the HBM rate for the norm at [8192, 8192].  Rows that
+  // are only quantised have twice the threads instead (71 against 75 us at
+  // [25600, 5120]).
+  constexpr bool kAhead = MODE != kRowQuant;
   __shared__ uint2 red[2][32];
   grid_dependency_wait();
   grid_dependency_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int nvec = P.d / VEC;
-  const raw* w_in = reinterpret_cast<const raw*>(P.weight);
-  raw w[NV];
-  if constexpr (MODE != kRowQuant) {
+  const long long first = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.y;
+  raw w[MODE != kRowQuant ? NV : 1];
+  auto load_weight = [&](long long row) {
+    const RowSpan<VEC, RAGGED> span(row, P.d);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      w[i] = c < nvec ? w_in[c] : RV::zero();
+      w[i] = c < span.vecs ? span.template weight<E>(P.weight, c) : RV::zero();
     }
-  }
-  const long long first = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.y;
+  };
+  if constexpr (kHoldWeight) load_weight(first);
+  const size_t total = static_cast<size_t>(P.rows) * P.d;
   int buf = 0;
+  raw x[NV], t[MODE == kRowNormAdd ? NV : 1];
+  auto load_row = [&](long long row) {
+    const RowSpan<VEC, RAGGED> span(row, P.d);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      x[i] = c < span.vecs ? span.template load<E>(P.x, c, total) : RV::zero();
+      if constexpr (MODE == kRowNormAdd)
+        t[i] = c < span.vecs ? span.template load<E>(P.residual, c, total) : RV::zero();
+    }
+  };
+  if (kAhead && first < P.rows) load_row(first);
   for (long long row = first; row < P.rows; row += stride) {
-    const size_t at = static_cast<size_t>(row) * P.d;
-    const raw* x = reinterpret_cast<const raw*>(static_cast<const E*>(P.x) + at);
-    const raw* r = MODE == kRowNormAdd
-                       ? reinterpret_cast<const raw*>(static_cast<const E*>(P.residual) + at)
-                       : nullptr;
+    const RowSpan<VEC, RAGGED> span(row, P.d);
+    if (!kAhead) load_row(row);
     raw h[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      h[i] = c < nvec ? x[c] : RV::zero();
-    }
-    if constexpr (MODE == kRowNormAdd) {
-      raw t[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        t[i] = c < nvec ? r[c] : RV::zero();
-      }
-      raw* ho = reinterpret_cast<raw*>(static_cast<E*>(P.h_out) + at);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        h[i] = row_h<E, VEC, MODE>(h[i], t[i]);
-        if (c < nvec) ho[c] = h[i];
+      h[i] = row_h<E, VEC, MODE>(x[i], t[MODE == kRowNormAdd ? i : 0]);
+      if (c < span.vecs) {
+        span.template own<E>(h[i], c);
+        if constexpr (MODE == kRowNormAdd) span.template store<E>(P.h_out, c, h[i]);
       }
     }
-    float sq = 0.f, inv, scale;
+    if (kAhead && row + stride < P.rows) load_row(row + stride);
+    if constexpr (MODE != kRowQuant && !kHoldWeight) load_weight(row);
+    float sq = 0.f;
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) row_stats<E, VEC, MODE>(h[i], w[i], sq, top);
+    for (int i = 0; i < NV; ++i)
+      row_stats<E, VEC, MODE>(h[i], w[MODE != kRowQuant ? i : 0], sq, top);
     row_reduce(sq, top, warps, warp, lane, red[buf]);
     buf ^= 1;  // the slots are written again two rows on, past a barrier
-    row_scale<MODE>(sq, top, P.d, P.eps, inv, scale);
-    if (threadIdx.x == 0) P.scale[row] = scale;
+    const float inv = row_inv<MODE>(sq, top);
+    if (threadIdx.x == 0) P.scale[row] = row_scale<MODE>(sq, top, inv, P.d, P.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nvec && DORA_BOUNDS_OK((c + 1) * VEC <= P.d && row < P.rows)) {
+      if (c < span.vecs && DORA_BOUNDS_OK(c * VEC + span.hi(c) - span.lead <= P.d)) {
         float u[VEC];
-        row_u<E, VEC, MODE>(h[i], w[i], u);
+        row_u<E, VEC, MODE>(h[i], w[MODE != kRowQuant ? i : 0], u);
         if (inv == 0.f) {  // also where u is not finite
 #pragma unroll
           for (int e = 0; e < VEC; ++e) u[e] = 0.f;
         }
-        store_codes<VEC>(P.q + at + static_cast<size_t>(c) * VEC, u, inv);
+        store_codes<VEC>(P.q + span.base + static_cast<size_t>(c) * VEC, u, inv, span.lo(c),
+                         span.hi(c));
       }
     }
   }
@@ -289,7 +453,7 @@ __global__ void __launch_bounds__(kRowThreads) row_quant_kernel(const RowArgs P)
 
 // Rows longer than the registers hold: two passes over the row, the second
 // from L2 (of h, as this thread stored it, where there is a residual).
-template <typename E, int VEC, int MODE>
+template <typename E, int VEC, int MODE, bool RAGGED>
 __global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowArgs P) {
   using RV = RowVec<E, VEC>;
   using raw = typename RV::raw;
@@ -297,37 +461,42 @@ __global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowAr
   grid_dependency_wait();
   grid_dependency_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int nvec = P.d / VEC;
-  const raw* w_in = reinterpret_cast<const raw*>(P.weight);
+  const size_t total = static_cast<size_t>(P.rows) * P.d;
   int buf = 0;
   for (long long row = blockIdx.x; row < P.rows; row += gridDim.x) {
-    const size_t at = static_cast<size_t>(row) * P.d;
-    const raw* x = reinterpret_cast<const raw*>(static_cast<const E*>(P.x) + at);
-    raw* ho = reinterpret_cast<raw*>(static_cast<E*>(P.h_out) + at);
-    float sq = 0.f, inv, scale;
+    const RowSpan<VEC, RAGGED> span(row, P.d);
+    auto weight = [&](int c) {
+      if constexpr (MODE == kRowQuant)
+        return RV::zero();
+      else
+        return span.template weight<E>(P.weight, c);
+    };
+    float sq = 0.f;
     uint32_t top = 0;
-    for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
-      raw h = x[c];
-      if constexpr (MODE == kRowNormAdd) {
-        h = row_h<E, VEC, MODE>(
-            h, reinterpret_cast<const raw*>(static_cast<const E*>(P.residual) + at)[c]);
-        ho[c] = h;
-      }
-      row_stats<E, VEC, MODE>(h, MODE != kRowQuant ? w_in[c] : RV::zero(), sq, top);
+    for (int c = threadIdx.x; c < span.vecs; c += blockDim.x) {
+      raw h = span.template load<E>(P.x, c, total);
+      if constexpr (MODE == kRowNormAdd)
+        h = row_h<E, VEC, MODE>(h, span.template load<E>(P.residual, c, total));
+      span.template own<E>(h, c);
+      if constexpr (MODE == kRowNormAdd) span.template store<E>(P.h_out, c, h);
+      row_stats<E, VEC, MODE>(h, weight(c), sq, top);
     }
     row_reduce(sq, top, warps, warp, lane, red[buf]);
     buf ^= 1;
-    row_scale<MODE>(sq, top, P.d, P.eps, inv, scale);
-    if (threadIdx.x == 0) P.scale[row] = scale;
-    for (int c = threadIdx.x; c < nvec; c += blockDim.x) {
-      const raw h = MODE == kRowNormAdd ? ho[c] : x[c];
+    const float inv = row_inv<MODE>(sq, top);
+    if (threadIdx.x == 0) P.scale[row] = row_scale<MODE>(sq, top, inv, P.d, P.eps);
+    for (int c = threadIdx.x; c < span.vecs; c += blockDim.x) {
+      raw h = span.template load<E>(MODE == kRowNormAdd ? P.h_out : P.x, c, total);
+      span.template own<E>(h, c);
       float u[VEC];
-      row_u<E, VEC, MODE>(h, MODE != kRowQuant ? w_in[c] : RV::zero(), u);
+      row_u<E, VEC, MODE>(h, weight(c), u);
       if (inv == 0.f) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) u[e] = 0.f;
       }
-      store_codes<VEC>(P.q + at + static_cast<size_t>(c) * VEC, u, inv);
+      if (DORA_BOUNDS_OK(c * VEC + span.hi(c) - span.lead <= P.d))
+        store_codes<VEC>(P.q + span.base + static_cast<size_t>(c) * VEC, u, inv, span.lo(c),
+                         span.hi(c));
     }
   }
 }
@@ -384,6 +553,60 @@ __global__ void __launch_bounds__(kStreamThreads)
                s[u];
       *reinterpret_cast<typename RowVec<E, VEC>::raw*>(x + static_cast<size_t>(r) * cols + c) =
           RowVec<E, VEC>::pack(o);
+    }
+  }
+}
+
+// The same for any number of columns, where the matrix is aligned as a whole:
+// vectors of the flat matrix, whose elements may belong to several rows.
+template <typename E, int VEC>
+__global__ void __launch_bounds__(kStreamThreads)
+    dequant_flat_kernel(const int8_t* q, const float* scale, long long rows, int cols, E* x) {
+  using raw = typename CodeVec<E, VEC>::raw;
+  constexpr int U = 4;
+  grid_dependency_wait();
+  grid_dependency_trigger();
+  const size_t total = static_cast<size_t>(rows) * cols;
+  const size_t step = static_cast<size_t>(gridDim.x) * kStreamThreads;
+  for (size_t j0 = static_cast<size_t>(blockIdx.x) * kStreamThreads + threadIdx.x;
+       j0 * VEC < total; j0 += step * U) {
+    raw v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const size_t i = (j0 + k * step) * VEC;
+      if (i + VEC <= total) v[k] = *reinterpret_cast<const raw*>(q + i);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const size_t i = (j0 + k * step) * VEC;
+      if (i >= total) break;
+      const size_t r = total <= 0xffffffffu
+                           ? static_cast<size_t>(static_cast<uint32_t>(i) /
+                                                 static_cast<uint32_t>(cols))
+                           : i / cols;
+      const int first = cols - static_cast<int>(i - r * cols);  // elements of row r
+      const int left = total - i < VEC ? static_cast<int>(total - i) : VEC;
+      const float s0 = scale[r];
+      float o[VEC];
+      if (first >= VEC && left == VEC) {  // one row's
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          o[e] = static_cast<float>(
+                     static_cast<int8_t>(code_word(v[k], e / 4) >> (8 * (e % 4)))) * s0;
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (e < left)
+            o[e] = static_cast<float>(q[i + e]) *
+                   (e < first ? s0 : scale[r + 1 + (e - first) / cols]);
+      }
+      if (left == VEC) {
+        *reinterpret_cast<typename RowVec<E, VEC>::raw*>(x + i) = RowVec<E, VEC>::pack(o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (e < left) x[i + e] = static_cast<E>(o[e]);
+      }
     }
   }
 }
