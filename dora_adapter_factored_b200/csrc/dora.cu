@@ -2391,8 +2391,8 @@ dora_status_t launch_pair_i8(const LinearPlan& p, const LinearArgs& A, const int
   P.kb = p.kb;
   P.tiles_m = p.tiles_m;
   P.tiles_n = p.tiles_n;
-  P.group = static_cast<int>(std::max<size_t>(
-      1, std::min<size_t>(p.tiles_n, kPairI8GroupBytes / (static_cast<size_t>(p.n) * ld))));
+  const size_t fit = std::max<size_t>(1, kPairI8GroupBytes / (static_cast<size_t>(p.n) * ld));
+  P.group = static_cast<int>(ceil_div_ll(p.tiles_n, ceil_div_ll(p.tiles_n, fit)));  // evened out
   P.idesc = idesc_i8_s32(2 * kI8M, p.n);
   const I8Ring r = plan_i8_ring(kPairI8MaxDynSmem - 1024,
                                 kI8WBytes + static_cast<size_t>(p.n / 2) * kI8K, p);

@@ -25,12 +25,10 @@ struct LinearArgs {
 };
 
 // fp32 value of one accumulated sum, the same operations in every kernel: the
-// conversion, one product with each scale, the bias in the second one's
-// rounding.
-__device__ __forceinline__ float linear_value(int acc, float sx, float sw, float bias,
-                                              bool has_bias) {
-  const float v = __fmul_rn(static_cast<float>(acc), sx);
-  return has_bias ? __fmaf_rn(v, sw, bias) : __fmul_rn(v, sw);
+// conversion, the product with the token's scale, and the product with the
+// channel's and the bias (+0 where there is none) in one rounding.
+__device__ __forceinline__ float linear_value(int acc, float sx, float sw, float bias) {
+  return __fmaf_rn(__fmul_rn(static_cast<float>(acc), sx), sw, bias);
 }
 
 __device__ __forceinline__ void linear_store(float* p, float v) { *p = v; }
@@ -82,7 +80,6 @@ __global__ void __launch_bounds__(kDotWarps * 32) dot_i8_kernel(const LinearArgs
 #pragma unroll
   for (int r = 0; r < kDotRows; ++r)
     wp[r] = P.wq + static_cast<size_t>(min(row0 + r, P.d_out - 1)) * P.d_in;
-  const bool has_bias = P.bias != nullptr;
   for (int t0 = static_cast<int>(blockIdx.y) * TT; t0 < P.T;
        t0 += static_cast<int>(gridDim.y) * TT) {
 #pragma unroll
@@ -140,7 +137,7 @@ __global__ void __launch_bounds__(kDotWarps * 32) dot_i8_kernel(const LinearArgs
         DORA_BOUNDS_OK(row >= 0 && tok >= 0)) {
       linear_store(static_cast<O*>(P.y) + static_cast<size_t>(tok) * P.d_out + row,
                    linear_value(mine, P.x_scale[tok], P.w_scale[row],
-                                has_bias ? P.bias[row] : 0.f, has_bias));
+                                P.bias != nullptr ? P.bias[row] : 0.f));
     }
     if (splits > 1) __syncthreads();  // before `part` is written again
   }
@@ -226,18 +223,17 @@ template <typename O>
 struct ChannelOut {
   O* y;  // the channel's column 0; where `pairs`, of the even channel of its pair
   float sw, bias;
-  bool ok, has_bias;
+  bool ok;
   bool pairs;  // bf16: channels 2i and 2i + 1 are stored together, 4 bytes aligned
   int T;
   long long d_out;
   // (made before the accumulator is waited for: the scale comes from memory)
   __device__ __forceinline__ ChannelOut(const LinearArgs& a, int row) {
     ok = row < a.d_out && DORA_BOUNDS_OK(row >= 0);
-    has_bias = a.bias != nullptr;
     pairs = sizeof(O) == 2 && a.d_out % 2 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 3) == 0;
     y = static_cast<O*>(a.y) + (pairs ? row & ~1 : row);
     sw = ok ? a.w_scale[row] : 0.f;
-    bias = ok && has_bias ? a.bias[row] : 0.f;
+    bias = ok && a.bias != nullptr ? a.bias[row] : 0.f;
     T = a.T;
     d_out = a.d_out;
   }
@@ -245,41 +241,41 @@ struct ChannelOut {
   // are read before any is stored: a load between the stores would have to
   // wait for them, since y might alias it.  bf16 values are rounded two to an
   // instruction and stored by pairs of channels: the even lane of a pair
-  // stores both channels of one column, the odd lane those of the next (one
-  // 2-byte store and one rounding per value made the epilogue of 128 columns
-  // 5.1 us).
+  // stores both channels of one column, the odd lane those of the next.  The
+  // instructions per column set the epilogue's time, so the cases of a full
+  // and a cut tile, of pairs and single channels, are apart.
   template <int N>
   __device__ __forceinline__ void put(int t, const int (&acc)[N], const float* sx) const {
     float s[N];
 #pragma unroll
     for (int c = 0; c < N; c += 4)
       *reinterpret_cast<float4*>(s + c) = *reinterpret_cast<const float4*>(sx + c);
-    O* p = y + t * d_out;
     const int left = ok ? T - t : 0;
-    if constexpr (sizeof(O) == 2) {
-      const bool odd = threadIdx.x & 1;
-      if (pairs) p += odd ? d_out : 0;
-#pragma unroll
-      for (int c = 0; c < N; c += 2) {
-        const uint32_t v =
-            pack_bf16x2_rn(linear_value(acc[c], s[c], sw, bias, has_bias),
-                           linear_value(acc[c + 1], s[c + 1], sw, bias, has_bias));
-        if (pairs) {
-          const uint32_t u = __shfl_xor_sync(0xffffffffu, v, 1);
-          if (c + (odd ? 1 : 0) < left)
-            *reinterpret_cast<uint32_t*>(p) =
-                odd ? __byte_perm(u, v, 0x7632) : __byte_perm(v, u, 0x5410);
-        } else {
-          uint16_t* h = reinterpret_cast<uint16_t*>(p);
-          if (c < left) h[0] = static_cast<uint16_t>(v);
-          if (c + 1 < left) h[d_out] = static_cast<uint16_t>(v >> 16);
-        }
-        p += 2 * d_out;
-      }
+    if (sizeof(O) == 2 && pairs) {
+      if (__all_sync(0xffffffffu, left >= N))
+        put_pairs<N, true>(t, acc, s, left);
+      else
+        put_pairs<N, false>(t, acc, s, left);
     } else {
+      O* p = y + t * d_out;
 #pragma unroll
       for (int c = 0; c < N; ++c, p += d_out)
-        if (c < left) *p = linear_value(acc[c], s[c], sw, bias, has_bias);
+        if (c < left) linear_store(p, linear_value(acc[c], s[c], sw, bias));
+    }
+  }
+  template <int N, bool FULL>
+  __device__ __forceinline__ void put_pairs(int t, const int (&acc)[N], const float (&s)[N],
+                                            int left) const {
+    const int odd = threadIdx.x & 1;
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;
+    O* p = y + (t + odd) * d_out;
+    left -= odd;
+#pragma unroll
+    for (int c = 0; c < N; c += 2, p += 2 * d_out) {
+      const uint32_t v = pack_bf16x2_rn(linear_value(acc[c], s[c], sw, bias),
+                                        linear_value(acc[c + 1], s[c + 1], sw, bias));
+      const uint32_t u = __shfl_xor_sync(0xffffffffu, v, 1);
+      if (FULL || c < left) *reinterpret_cast<uint32_t*>(p) = __byte_perm(v, u, pick);
     }
   }
 };
