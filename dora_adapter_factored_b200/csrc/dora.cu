@@ -2173,7 +2173,15 @@ int padded_k(int64_t d_in) { return static_cast<int>(align_up(static_cast<size_t
 size_t linear_pad_x(int64_t T, int64_t d_in) {
   return align_up(static_cast<size_t>(T) * padded_k(d_in), 256);
 }
-bool linear_pads(int64_t T, int64_t d_in) { return T > kDotMaxT && d_in % 16 != 0; }
+// (Small products of such rows are dot products, which need no copies: 4.1
+// against 5.7 us for one token at 1001 x 1003, but 15.4 against 9.4 at 376 x
+// 11963 and 72 against 31 at 14336 x 4097.)
+constexpr int64_t kDotRaggedMacs = int64_t(4) << 20;
+constexpr int64_t kDotRaggedK = 4096;
+bool linear_pads(int64_t T, int64_t d_out, int64_t d_in) {
+  return d_in % 16 != 0 &&
+         (T > kDotMaxT || d_in > kDotRaggedK || d_out > kDotRaggedMacs / (T * d_in));
+}
 
 // Launch with the cluster size of the call and programmatic serialization.
 template <typename... KArgs, typename... Args>
@@ -2418,16 +2426,16 @@ dora_status_t launch_pair_i8(const LinearPlan& p, const LinearArgs& A, const int
 template <typename O>
 dora_status_t launch_linear(const LinearArgs& A, void* ws, const DeviceInfo& d, cudaStream_t cs) {
   const bool vec = A.d_in % 16 == 0 && aligned16(A.xq) && aligned16(A.wq);
-  const bool pads = linear_pads(A.T, A.d_in);
+  const bool pads = linear_pads(A.T, A.d_out, A.d_in);
   double us = 0.0;
   LinearPlan p{};
   if (vec || pads) p = plan_linear(A.T, A.d_out, A.d_in, d, &us);
-  // Dot products: few tokens, where they are faster or rows are not of whole
-  // 16-byte steps; any number where rows are, but start off a boundary (TMA
-  // cannot read those, and the workspace, sized from the shape, has no room
-  // for copies).
-  const bool few = A.T <= kDotMaxT &&
-                   (!vec || estimate_dot_us(A.T, A.d_out, A.d_in) < us);
+  // Dot products: few tokens, where they are faster; rows that are not of whole
+  // 16-byte steps, where few; and any number of rows that are, but start off a
+  // boundary (TMA cannot read those, and the workspace, sized from the shape,
+  // has no room for copies).
+  const bool few =
+      vec && A.T <= kDotMaxT && estimate_dot_us(A.T, A.d_out, A.d_in) < us;
   if (few || (!vec && !pads)) {
     launch_dot_any<O>(A, vec, d.sms, cs);
     return launch_status();
@@ -2504,7 +2512,7 @@ dora_status_t dora_rmsnorm_quant(const void* x, const void* residual, const void
 
 size_t dora_linear_i8_workspace_size(int64_t T, int64_t d_out, int64_t d_in) {
   if (T < 1 || d_out < 1 || d_in < 1 || T > kMaxLinearTokens || d_out > kMaxQuantRows ||
-      d_in > DORA_MAX_I8_K || !linear_pads(T, d_in))
+      d_in > DORA_MAX_I8_K || !linear_pads(T, d_out, d_in))
     return 0;
   return linear_pad_x(T, d_in) + linear_pad_x(d_out, d_in);
 }

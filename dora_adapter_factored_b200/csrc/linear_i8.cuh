@@ -62,8 +62,25 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int c) {
   return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), c);
 }
 
+// Four codes from any address as a word: put together from the two aligned
+// words they lie in where both are inside [begin, end), else byte by byte, of
+// which the first `n` are read and the others zero.
+__device__ __forceinline__ uint32_t load4_any(const int8_t* p, int n, uintptr_t begin,
+                                              uintptr_t end) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p), lo = at & ~static_cast<uintptr_t>(3);
+  if (n >= 4 && lo >= begin && lo + 8 <= end) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(lo);
+    return __funnelshift_r(w[0], w[1], static_cast<uint32_t>(at & 3) * 8);
+  }
+  uint32_t v = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    if (b < n) v |= (static_cast<uint32_t>(p[b]) & 0xffu) << (8 * b);
+  return v;
+}
+
 // VEC16: rows of both operands start at 16-byte boundaries and d_in is a
-// multiple of 16; otherwise bytes.
+// multiple of 16; otherwise rows start at any byte.
 template <typename O, int TT, bool VEC16>
 __global__ void __launch_bounds__(kDotWarps * 32) dot_i8_kernel(const LinearArgs P, int splits) {
   static_assert(kDotRows * TT <= 32, "one lane per result");
@@ -104,16 +121,22 @@ __global__ void __launch_bounds__(kDotWarps * 32) dot_i8_kernel(const LinearArgs
         }
       }
     } else {
-#pragma unroll 4
-      for (int k = slice * 32 + lane; k < P.d_in; k += splits * 32) {
-        int w[kDotRows];
+      const uintptr_t w0 = reinterpret_cast<uintptr_t>(P.wq);
+      const uintptr_t w1 = w0 + static_cast<uintptr_t>(P.d_out) * P.d_in;
+      const uintptr_t x0 = reinterpret_cast<uintptr_t>(P.xq);
+      const uintptr_t x1 = x0 + static_cast<uintptr_t>(P.T) * P.d_in;
+#pragma unroll 2
+      for (int k = (slice * 32 + lane) * 4; k < P.d_in; k += splits * 128) {
+        const int n = P.d_in - k;
+        uint32_t w[kDotRows];
 #pragma unroll
-        for (int r = 0; r < kDotRows; ++r) w[r] = wp[r][k];
+        for (int r = 0; r < kDotRows; ++r) w[r] = load4_any(wp[r] + k, n, w0, w1);
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const int x = xp[t][k];
+          const uint32_t x = load4_any(xp[t] + k, n, x0, x1);
 #pragma unroll
-          for (int r = 0; r < kDotRows; ++r) acc[r][t] += w[r] * x;
+          for (int r = 0; r < kDotRows; ++r)
+            acc[r][t] = __dp4a(static_cast<int>(w[r]), static_cast<int>(x), acc[r][t]);
         }
       }
     }
@@ -283,6 +306,7 @@ struct ChannelOut {
 // Epilogue warps of a CTA: two per quarter of the TMEM lanes (a warp reads the
 // quarter of its index modulo 4), which take the 16-column groups in turn.
 constexpr int kI8EpiWarps = 8;
+constexpr int kI8ColStep = 16 * (kI8EpiWarps / 4);  // from a warp's group of 16 to its next
 
 // Calls f(c, v) with this warp's groups of 16 among the n accumulator columns
 // (a multiple of 16) from `tmem`, the next group on its way meanwhile.
@@ -292,15 +316,15 @@ __device__ __forceinline__ void for_columns(uint32_t tmem, int n, int warp, F&& 
   if (c >= n) return;
   int a[16], b[16];
   tmem_load_16cols(tmem + c, a);
-  for (; c < n; c += 64) {
+  for (; c < n; c += 2 * kI8ColStep) {
     tmem_wait_16cols(a);
-    if (c + 32 < n) tmem_load_16cols(tmem + c + 32, b);
+    if (c + kI8ColStep < n) tmem_load_16cols(tmem + c + kI8ColStep, b);
     f(c, a);
     __syncwarp();
-    if (c + 32 < n) {
+    if (c + kI8ColStep < n) {
       tmem_wait_16cols(b);
-      if (c + 64 < n) tmem_load_16cols(tmem + c + 64, a);
-      f(c + 32, b);
+      if (c + 2 * kI8ColStep < n) tmem_load_16cols(tmem + c + 2 * kI8ColStep, a);
+      f(c + kI8ColStep, b);
       __syncwarp();
     }
   }
@@ -363,13 +387,13 @@ __device__ __forceinline__ void i8_finish_columns(const ChannelOut<O>& out, cons
   };
   const uint32_t own = lane_base + static_cast<uint32_t>(slice * cols);
   const int whole = cols & ~15;
-  for (int c = (warp >> 2) * 16; c < whole; c += 32) {
+  for (int c = (warp >> 2) * 16; c < whole; c += kI8ColStep) {
     int sum[16];
     tmem_load_16cols(own + c, sum);
     tmem_wait_16cols(sum);
     group(sum, c);
   }
-  for (int c = whole + (warp >> 2) * 4; c < cols; c += 8) {
+  for (int c = whole + (warp >> 2) * 4; c < cols; c += kI8EpiWarps) {
     int sum[4];
     tmem_load_4cols_wait(own + c, sum);
     group(sum, c);
@@ -725,7 +749,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
         if (*abort_flag != 0) out.ok = false;
         const uint32_t acc = lane_base + static_cast<uint32_t>(b * kI8MaxN);
         for_columns(acc, P.n, warp, [&](int c, const int(&v)[16]) {
-          if (c + 32 >= P.n) {  // this warp's last columns are in registers: hand it back
+          if (c + kI8ColStep >= P.n) {  // this warp's last columns are in registers: hand it back
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
