@@ -2226,14 +2226,16 @@ struct LinearPlan {
   int n, tiles_m, tiles_n, splits, kb;
 };
 
-// Two CTAs share an SM where there are more CTAs than SMs, and where a CTA has
-// few k-blocks, so that the next launch can set itself up beside it (24 tokens
-// at 4096 x 4096, split four ways: 5.8 us against 6.9 us).
-constexpr int kTileI8ShortK = 8;
+// Two CTAs share an SM where there are more CTAs than SMs.
 bool tile_i8_shares_sm(const LinearPlan& p, int sms) {
-  return static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits > sms ||
-         ceil_div_ll(p.kb, p.splits) <= kTileI8ShortK;
+  return static_cast<long long>(p.tiles_m) * p.tiles_n * p.splits > sms;
 }
+
+// k-blocks of the weight per SM that a CTA (or the two that share it) brings
+// into L2 early: 256 KiB.  24 or more cost what the kernel before still reads;
+// CTAs of up to 8 k-blocks have them on their way at once anyway.
+constexpr int kTileI8Ahead = 16;
+constexpr int kTileI8ShortK = 8;
 
 // Estimated time of a plan in us; negative where a split k would not have all
 // its clusters resident at once (a second wave costs more than a split gains).
@@ -2365,6 +2367,9 @@ dora_status_t launch_tile_i8(const LinearPlan& p, const LinearArgs& A, const int
   const size_t dyn = tile_i8_shares_sm(p, sms) ? (size_t(113) << 10) - sizeof(TileI8Tail) : kTileI8MaxDynSmem;
   const I8Ring r = plan_i8_ring(dyn - 1024, kI8WBytes + static_cast<size_t>(p.n) * kI8K, p);
   P.stages = r.stages;
+  P.ahead = ceil_div_ll(p.kb, p.splits) <= kTileI8ShortK
+                ? 0
+                : kTileI8Ahead / (tile_i8_shares_sm(p, sms) ? 2 : 1);
   P.part_off = r.part_off;
   P.part_over_ring = r.part_over_ring;
   const size_t used = r.bytes;

@@ -413,6 +413,7 @@ struct alignas(64) TileI8Dev {
   int n;             // tokens per tile
   int kb;            // k-blocks
   int stages;
+  int ahead;         // k-blocks of the weight to bring into L2 early
   uint32_t part_off; // of the partials, from the ring's start
   int part_over_ring;
   uint32_t tmem_cols, idesc;
@@ -468,6 +469,14 @@ __global__ void __launch_bounds__(kTileI8Threads)
     __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = tail.tmem_slot;
+  // The weight's first k-blocks come into L2 while the kernel before this one
+  // still runs (a prefetch reads nothing, so the weight may even be its
+  // output): 12.8 instead of 13.9 us per call for 24 tokens at 8192 x 8192, 14.7
+  // instead of 16.8 with the norm before each.
+  if (warp == 0 && elect_one())
+    for (int k = kb0; k < min(kb1, kb0 + P.ahead); ++k)
+      tma_prefetch_2d(&P.tm_w, k * kI8K, row0);
+  __syncwarp();
   grid_dependency_wait();
   grid_dependency_trigger();  // not before TMEM is held: the next grid may want it too
 
