@@ -2244,7 +2244,7 @@ constexpr int kTileI8ShortK = 8;
 // pays its set-up, the epilogue of its columns and, with a split k, the
 // exchange of partials.  The constants are a fit to the measured times of all
 // plans on 12 weights from 512 x 512 to 25600 x 5120 at 4 to 1500 tokens (2600
-// plans); the plan it picks is on average 1 to 2 % slower than the fastest,
+// plans); the plan it picks is on average 1 % slower than the fastest,
 // where a fixed rule (pairs above 64 tokens with the widest tile) was 20 %
 // slower.
 double estimate_linear_us(const LinearPlan& p, long long T, long long d_out, long long d_in,
@@ -2253,31 +2253,31 @@ double estimate_linear_us(const LinearPlan& p, long long T, long long d_out, lon
   const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
   const double kbs = static_cast<double>(ceil_div_ll(p.kb, p.splits));
   const double stage_kb = (kI8WBytes + (p.pair ? p.n / 2 : p.n) * kI8K) / 1000.0;
-  const double exchange = p.splits > 1 ? 0.14 + 0.04 * n * (S - 1) / S : 0.0;
+  const double exchange = p.splits > 1 ? 0.19 + 0.0254 * n * (S - 1) / S : 0.0;
   const int cluster = (p.pair ? 2 : 1) * p.splits;
   long long slots = cluster == 8   ? d.clusters8
                     : cluster == 4 ? d.clusters4
                                    : std::max(1, d.sms / cluster);
   double base, kblock, epilogue;
   if (p.pair) {
-    base = 5.15;
-    kblock = std::max({stage_kb / 162.0, 0.00107 * n, 0.099});
-    epilogue = 0.0053 * n / S;
+    base = 4.43;
+    kblock = std::max({stage_kb / 173.0, 0.00111 * n, 0.141});
+    epilogue = 0.0047 * n / S;
   } else {
-    base = 2.02;
+    base = 2.07;
     if (tiles * p.splits > d.sms) slots *= 2;
     const bool two = std::min(tiles, slots) * p.splits > d.sms;  // CTAs on an SM
-    kblock = two ? std::max({stage_kb / 52.0, 0.0035 * n, 0.223})
-                 : std::max({stage_kb / 162.0, 0.00174 * n, 0.223});
-    epilogue = 0.355 + 0.0066 * n / S;
+    kblock = two ? std::max({stage_kb / 53.3, 0.0049 * n, 0.21})
+                 : std::max({stage_kb / 173.0, 0.00247 * n, 0.21});
+    epilogue = 0.395 + 0.0072 * n / S;
   }
   const long long full = tiles / slots, rest = tiles % slots;
   if (p.splits > 1 && full + (rest > 0) > 1) return -1.0;
   const double moved = static_cast<double>(d_out + T) * d_in / 1e6;  // MB from HBM
   const double l2 = tiles * (p.pair ? 2.0 : 1.0) * p.kb * stage_kb / 1000.0;
-  const double stream = std::max(moved / 6.63, l2 / 27.5) / tiles;  // us per tile
-  const double wave = std::max(kbs * kblock, 0.44 + stream * slots);
-  const double last = rest > 0 ? std::max(kbs * kblock, 0.44 + stream * rest) : 0.0;
+  const double stream = std::max(moved / 6.38, l2 / 24.2) / tiles;  // us per tile
+  const double wave = std::max(kbs * kblock, 0.31 + stream * slots);
+  const double last = rest > 0 ? std::max(kbs * kblock, 0.31 + stream * rest) : 0.0;
   // (two CTAs on an SM, or the two accumulators of a pair, hide most of the
   // epilogues but the last)
   const double waves = static_cast<double>(full + (rest > 0));
@@ -2316,11 +2316,11 @@ LinearPlan plan_linear(int T, int d_out, int d_in, const DeviceInfo& d, double* 
 }
 
 // Estimated time of the dot-product kernel: its stream of the weight slows
-// with the tokens (TB/s at 1, 2, 4 and 8: 5.0, 4.9, 4.0, 3.2 against 6.6 on the
+// with the tokens (TB/s at 1, 2, 4 and 8: 5.0, 4.9, 4.3, 3.2 against 6.4 on the
 // tensor cores), but it has nothing to set up (1024 x 4096: 2.7 us at one
 // token and 3.8 at eight, against 4.6; 14336 x 4096 at one: 13.7 against 12.5).
 double estimate_dot_us(long long T, long long d_out, long long d_in) {
-  const double tbs = T == 1 ? 5.0 : T == 2 ? 4.9 : T <= 4 ? 4.0 : 3.2;
+  const double tbs = T == 1 ? 5.0 : T == 2 ? 4.9 : T <= 4 ? 4.3 : 3.2;
   return 2.1 + static_cast<double>(d_out) * d_in / 1e6 / tbs;
 }
 
