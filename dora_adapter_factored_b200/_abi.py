@@ -744,7 +744,8 @@ def dora_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float,
         raise ValueError("h_out is the sum with a residual: pass residual too")
     q, pq = _out_matrix(q, "q", x, _I8, index, stream)
     scale, ps = _out_vector(scale, "scale", x, T, _F32, index, stream)
-    status = lib.dora_rmsnorm_quant(px, pr, pw, eps, dt, T, d, ph, pq, ps, _current(stream, index))
+    status = lib.dora_rmsnorm_quant(px, pr, pw, float(eps), dt, T, d, ph, pq, ps,
+                                    _current(stream, index))
     if status:
         raise DoraError(status, "dora_rmsnorm_quant")
     return q, scale, h_out
@@ -763,8 +764,9 @@ def dora_linear_i8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor,
     int8; scales and bias fp32."""
     lib = _lib or load_library()
     index = _here(xq, "xq")
-    _here(wq, "wq")
     T, d_in = shape = xq.shape
+    if not isinstance(wq, torch.Tensor) or wq.dim() != 2:
+        raise ValueError("wq must be a torch.Tensor of two dimensions")
     d_out = wq.shape[0]
     px = _arg(xq, "xq", _I8, shape, index)
     psx = _arg(x_scale, "x_scale", _F32, (T,), index)
@@ -779,10 +781,10 @@ def dora_linear_i8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor,
         py = _arg(y, "y", dtype, (T, d_out), index)
     else:
         if stream is None:
-            y = xq.new_empty((T, d_out), dtype=dtype)
+            y = torch.empty(T, d_out, dtype=dtype, device=xq.device)
         else:
             with _on_stream(stream, xq):
-                y = xq.new_empty((T, d_out), dtype=dtype)
+                y = torch.empty(T, d_out, dtype=dtype, device=xq.device)
         py = y.data_ptr()
     pws, nws = None, 0
     if ws is not None:

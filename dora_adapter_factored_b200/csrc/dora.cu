@@ -167,7 +167,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // split with room for one CTA per SM (the [8192, 25600] backward went from
 // 347 to 446 us).  It is a hint: if the runtime refuses it, the launch goes
 // ahead without it.
-void prefer_l1(const void* kernel) {
+void prefer_l1(const void* kernel, int ctas) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -189,7 +189,7 @@ void prefer_l1(const void* kernel) {
     (void)cudaGetLastError();
     return;
   }
-  const long long need = static_cast<long long>(kStreamCtasPerSm) *
+  const long long need = static_cast<long long>(ctas) *
                          (static_cast<long long>(fa.sharedSizeBytes) + reserve);
   const int percent =
       static_cast<int>(std::min<long long>(100, (100 * need + sm_smem - 1) / sm_smem));
@@ -203,7 +203,7 @@ void prefer_l1(const void* kernel) {
 template <typename... KArgs, typename... Args>
 cudaError_t launch_stream(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                           cudaStream_t st, Args&&... args) {
-  prefer_l1(reinterpret_cast<const void*>(kernel));
+  prefer_l1(reinterpret_cast<const void*>(kernel), kStreamCtasPerSm);
   return launch_pdl(kernel, grid, block, smem, st, std::forward<Args>(args)...);
 }
 
@@ -2020,6 +2020,10 @@ constexpr int64_t kMaxQuantRows = int64_t(1) << 30;
 constexpr int64_t kMaxQuantCols = int64_t(1) << 30;
 constexpr int64_t kMaxLinearTokens = int64_t(1) << 23;  // token tiles are a grid's second axis
 
+// The most blocks an SM holds of any launch of the row kernels (64 threads of
+// 64 registers): their L1/shared split has room for them.
+constexpr int kRowMaxCtasPerSm = 16;
+
 template <typename E, int VEC, int NV, int MODE, bool RAGGED>
 void launch_rows_nv(const RowArgs& P, long long nvec, int sms, cudaStream_t cs) {
   const long long want = ceil_div_ll(ceil_div_ll(nvec, NV), 32) * 32;
@@ -2032,10 +2036,14 @@ void launch_rows_nv(const RowArgs& P, long long nvec, int sms, cudaStream_t cs) 
   long long grid = static_cast<long long>(sms) * per_sm;
   if (RAGGED && grid * by % VEC != 0) grid = std::max<long long>(VEC, grid / VEC * VEC);
   const dim3 blocks(static_cast<unsigned>(std::min(groups, grid)));
+  auto go = [&](auto kernel) {
+    prefer_l1(reinterpret_cast<const void*>(kernel), kRowMaxCtasPerSm);
+    launch_pdl(kernel, blocks, dim3(threads, by), 0, cs, P);
+  };
   if (fits)
-    launch_stream(row_quant_kernel<E, VEC, NV, MODE, RAGGED>, blocks, dim3(threads, by), 0, cs, P);
+    go(row_quant_kernel<E, VEC, NV, MODE, RAGGED>);
   else
-    launch_stream(row_quant_long_kernel<E, VEC, MODE, RAGGED>, blocks, dim3(threads), 0, cs, P);
+    go(row_quant_long_kernel<E, VEC, MODE, RAGGED>);
 }
 
 template <typename E, int VEC, int MODE, bool RAGGED>
@@ -2200,11 +2208,16 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) {
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) {  // as launch_pdl: plain stream order
     (void)cudaGetLastError();
-    note_error("cluster launch", e);
-    launch_failed = true;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();
+      note_error("cluster launch", e);
+      launch_failed = true;
+    }
   }
   return e;
 }

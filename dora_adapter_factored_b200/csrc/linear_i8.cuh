@@ -629,6 +629,7 @@ __global__ void __launch_bounds__(kPairI8Threads)
   const int step = static_cast<int>(gridDim.x) / (2 * S);
   auto give_up = [&] {
     st_cluster_u32(peer_abort, 1u);
+    fence_cluster();  // there before this thread's part in the last barrier
     linear_give_up(abort_flag);
   };
 
@@ -758,7 +759,10 @@ __global__ void __launch_bounds__(kPairI8Threads)
         if (*abort_flag != 0) out.ok = false;
         const uint32_t acc = lane_base + static_cast<uint32_t>(b * kI8MaxN);
         for_columns(acc, P.n, warp, [&](int c, const int(&v)[16]) {
-          if (c + kI8ColStep >= P.n) {  // this warp's last columns are in registers: hand it back
+          // This warp's last columns are in registers: hand it back (to the tile
+          // after the next; where there is none, nobody waits for it, and no
+          // arrival is on its way to a CTA that has left).
+          if (c + kI8ColStep >= P.n && i + 2 * step < tiles) {
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)

@@ -508,6 +508,10 @@ __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+__device__ __forceinline__ void fence_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
 // Every thread of the cluster, ordering no memory accesses: for CTAs that only
 // must not leave before the others are done.
 __device__ __forceinline__ void cluster_sync_relaxed() {
