@@ -29,6 +29,37 @@ constexpr float kCodeMax = 127.f;
 constexpr float kMinNormal = 1.17549435e-38f;  // 2^-126
 constexpr uint32_t kInfBits = 0x7f800000u;
 
+// Pairs of fp32 values in one instruction (each rounded as alone).
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split_f32(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// max(a, |b|, |c|), NaN if any is.
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+
 enum RowMode : int {
   kRowQuant = 0,    // x -> codes
   kRowNorm = 1,     // rms norm of x -> codes
@@ -146,17 +177,33 @@ __device__ __forceinline__ void store_part(E* p, const typename RowVec<E, VEC>::
     if (e >= lo && e < hi) p[e] = static_cast<E>(v[e]);
 }
 
-// The codes of VEC values: rint(u inv), half to even.  |u inv| <= 127 up to
-// two roundings, so the nearest integer is at most 127.
+// The codes of VEC values: u inv rounded to an integer, half to even, by the
+// addition of 1.5 2^23 in the product's rounding, which leaves the code in the
+// low byte (a conversion instruction has a quarter of the rate, and was the
+// longest part of the kernel's arithmetic).  |u inv| is at most 127 up to a
+// rounding of inv, so the nearest integer is at most 127.
+constexpr float kRoundMagic = 12582912.f;
+
 template <int VEC>
 __device__ __forceinline__ void store_codes(int8_t* p, const float (&u)[VEC], float inv, int lo,
                                             int hi) {
-  uint32_t w[(VEC + 3) / 4];
+  uint32_t q[VEC], w[(VEC + 3) / 4];
+  if constexpr (VEC > 1) {
+    const uint64_t inv2 = pair_f32(inv, inv), magic2 = pair_f32(kRoundMagic, kRoundMagic);
 #pragma unroll
-  for (int i = 0; i < (VEC + 3) / 4; ++i) w[i] = 0;
+    for (int e = 0; e < VEC; e += 2) {
+      float a, b;
+      split_f32(fma_f32x2(pair_f32(u[e], u[e + 1]), inv2, magic2), a, b);
+      q[e] = __float_as_uint(a);
+      q[e + 1] = __float_as_uint(b);
+    }
 #pragma unroll
-  for (int e = 0; e < VEC; ++e)
-    w[e / 4] |= (static_cast<uint32_t>(__float2int_rn(u[e] * inv)) & 0xffu) << (8 * (e % 4));
+    for (int i = 0; i < VEC / 4; ++i)
+      w[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040),
+                         __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040), 0x5410);
+  } else {
+    w[0] = __float_as_uint(__fmaf_rn(u[0], inv, kRoundMagic));
+  }
   if (lo > 0 || hi < VEC) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
@@ -276,33 +323,46 @@ __device__ __forceinline__ void row_u(const typename RowVec<E, VEC>::raw& h,
   if constexpr (MODE != kRowQuant) {
     float g[VEC];
     RV::unpack(w, g);
+    if constexpr (VEC > 1) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) u[e] *= g[e];
+      for (int e = 0; e < VEC; e += 2)
+        split_f32(mul_f32x2(pair_f32(u[e], u[e + 1]), pair_f32(g[e], g[e + 1])), u[e], u[e + 1]);
+    } else {
+      u[0] *= g[0];
+    }
   }
 }
 
-// One vector's share of the row's sum of squares and maximum.  The maximum is
-// taken over the bit patterns of |u|, which order like the values and put
-// infinities and NaN on top.
+// One vector's share of the row's sum of squares (two partial sums) and
+// maximum, which is NaN if a value is.
 template <typename E, int VEC, int MODE>
 __device__ __forceinline__ void row_stats(const typename RowVec<E, VEC>::raw& h,
-                                          const typename RowVec<E, VEC>::raw& w, float& sq,
-                                          uint32_t& top) {
+                                          const typename RowVec<E, VEC>::raw& w, uint64_t& sq,
+                                          float& top) {
   float u[VEC];
   row_u<E, VEC, MODE>(h, w, u);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) top = max(top, __float_as_uint(u[e]) & 0x7fffffffu);
+  for (int e = 0; e < VEC; e += 2) top = max_abs_nan(top, u[e], u[VEC > 1 ? e + 1 : e]);
   if constexpr (MODE != kRowQuant) {
     RowVec<E, VEC>::unpack(h, u);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) sq = fmaf(u[e], u[e], sq);
+    for (int e = 0; e < VEC; e += 2) {
+      const uint64_t v = pair_f32(u[e], VEC > 1 ? u[VEC > 1 ? e + 1 : e] : 0.f);
+      sq = fma_f32x2(v, v, sq);
+    }
   }
 }
 
 // Sum and maximum over the `warps` warps of a row's group, in a fixed order;
 // the same value in every thread.  `red`: the group's slots (two per warp).
-__device__ __forceinline__ void row_reduce(float& sq, uint32_t& top, int warps, int warp, int lane,
-                                           uint2* red) {
+__device__ __forceinline__ void row_reduce(uint64_t sq2, float top1, int warps, int warp, int lane,
+                                           uint2* red, float& sq, uint32_t& top) {
+  float a, b;
+  split_f32(sq2, a, b);
+  sq = a + b;
+  // As bit patterns, which order like the values (they are not negative) with
+  // infinity and NaN on top.
+  top = __float_as_uint(top1);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
   top = __reduce_max_sync(0xffffffffu, top);
@@ -425,12 +485,13 @@ __global__ void __maxnreg__(row_regs(MODE, NV)) row_quant_kernel(const RowArgs P
     }
     if (kAhead && row + stride < P.rows) load_row(row + stride);
     if constexpr (MODE != kRowQuant && !kHoldWeight) load_weight(row);
-    float sq = 0.f;
-    uint32_t top = 0;
+    uint64_t sq2 = 0;
+    float top1 = 0.f, sq;
+    uint32_t top;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      row_stats<E, VEC, MODE>(h[i], w[MODE != kRowQuant ? i : 0], sq, top);
-    row_reduce(sq, top, warps, warp, lane, red[buf]);
+      row_stats<E, VEC, MODE>(h[i], w[MODE != kRowQuant ? i : 0], sq2, top1);
+    row_reduce(sq2, top1, warps, warp, lane, red[buf], sq, top);
     buf ^= 1;  // the slots are written again two rows on, past a barrier
     const float inv = row_inv<MODE>(sq, top);
     if (threadIdx.x == 0) P.scale[row] = row_scale<MODE>(sq, top, inv, P.d, P.eps);
@@ -471,17 +532,18 @@ __global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowAr
       else
         return span.template weight<E>(P.weight, c);
     };
-    float sq = 0.f;
-    uint32_t top = 0;
+    uint64_t sq2 = 0;
+    float top1 = 0.f, sq;
+    uint32_t top;
     for (int c = threadIdx.x; c < span.vecs; c += blockDim.x) {
       raw h = span.template load<E>(P.x, c, total);
       if constexpr (MODE == kRowNormAdd)
         h = row_h<E, VEC, MODE>(h, span.template load<E>(P.residual, c, total));
       span.template own<E>(h, c);
       if constexpr (MODE == kRowNormAdd) span.template store<E>(P.h_out, c, h);
-      row_stats<E, VEC, MODE>(h, weight(c), sq, top);
+      row_stats<E, VEC, MODE>(h, weight(c), sq2, top1);
     }
-    row_reduce(sq, top, warps, warp, lane, red[buf]);
+    row_reduce(sq2, top1, warps, warp, lane, red[buf], sq, top);
     buf ^= 1;
     const float inv = row_inv<MODE>(sq, top);
     if (threadIdx.x == 0) P.scale[row] = row_scale<MODE>(sq, top, inv, P.d, P.eps);
@@ -519,6 +581,25 @@ __device__ __forceinline__ uint32_t code_word(const uint2& r, int i) { return i 
 __device__ __forceinline__ uint32_t code_word(uint32_t r, int) { return r; }
 __device__ __forceinline__ uint32_t code_word(uint8_t r, int) { return r; }
 
+// The VEC codes of r times s.  A code plus 128, in the low byte of 2^23, is the
+// number 2^23 + 128 + code: two exact additions away from a conversion
+// instruction's result, at four times its rate.
+template <int VEC, typename R>
+__device__ __forceinline__ void code_values(const R& r, float s, float (&o)[VEC]) {
+  if constexpr (VEC == 1) {
+    o[0] = static_cast<float>(static_cast<int8_t>(code_word(r, 0))) * s;
+  } else {
+    const uint64_t s2 = pair_f32(s, s), off2 = pair_f32(-8388736.f, -8388736.f);
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      const uint32_t w = code_word(r, e / 4) ^ 0x80808080u;
+      const float a = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 + e % 4));
+      const float b = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 + (e + 1) % 4));
+      split_f32(mul_f32x2(add_f32x2(pair_f32(a, b), off2), s2), o[e], o[e + 1]);
+    }
+  }
+}
+
 template <typename E, int VEC>
 __global__ void __launch_bounds__(kStreamThreads)
     dequant_rows_kernel(const int8_t* q, const float* scale, long long rows, int cols, E* x,
@@ -547,10 +628,7 @@ __global__ void __launch_bounds__(kStreamThreads)
       const long long r = r0 + u * step;
       if (r >= rows || !DORA_BOUNDS_OK(c + VEC <= cols)) continue;
       float o[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        o[e] = static_cast<float>(static_cast<int8_t>(code_word(v[u], e / 4) >> (8 * (e % 4)))) *
-               s[u];
+      code_values<VEC>(v[u], s[u], o);
       *reinterpret_cast<typename RowVec<E, VEC>::raw*>(x + static_cast<size_t>(r) * cols + c) =
           RowVec<E, VEC>::pack(o);
     }
@@ -589,10 +667,7 @@ __global__ void __launch_bounds__(kStreamThreads)
       const float s0 = scale[r];
       float o[VEC];
       if (first >= VEC && left == VEC) {  // one row's
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          o[e] = static_cast<float>(
-                     static_cast<int8_t>(code_word(v[k], e / 4) >> (8 * (e % 4)))) * s0;
+        code_values<VEC>(v[k], s0, o);
       } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
