@@ -185,8 +185,8 @@ __device__ __forceinline__ void store_part(E* p, const typename RowVec<E, VEC>::
 constexpr float kRoundMagic = 12582912.f;
 
 template <int VEC>
-__device__ __forceinline__ void store_codes(int8_t* p, const float (&u)[VEC], float inv, int lo,
-                                            int hi) {
+__device__ __forceinline__ void store_codes(int8_t* p, const float (&u)[VEC], float inv, bool part,
+                                            int lo, int hi) {
   uint32_t q[VEC], w[(VEC + 3) / 4];
   if constexpr (VEC > 1) {
     const uint64_t inv2 = pair_f32(inv, inv), magic2 = pair_f32(kRoundMagic, kRoundMagic);
@@ -204,7 +204,7 @@ __device__ __forceinline__ void store_codes(int8_t* p, const float (&u)[VEC], fl
   } else {
     w[0] = __float_as_uint(__fmaf_rn(u[0], inv, kRoundMagic));
   }
-  if (lo > 0 || hi < VEC) {
+  if (part) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
       if (e >= lo && e < hi) p[e] = static_cast<int8_t>(w[e / 4] >> (8 * (e % 4)));
@@ -246,38 +246,42 @@ template <int VEC, bool RAGGED>
 struct RowSpan {
   size_t base;
   int lead, vecs, d;
-  __device__ __forceinline__ RowSpan(long long row, int cols) {
+  bool end;  // the matrix's last row: its last vector may reach past the matrix
+  __device__ __forceinline__ RowSpan(long long row, int cols, long long rows) {
     const size_t at = static_cast<size_t>(row) * cols;
     lead = RAGGED ? static_cast<int>(at % VEC) : 0;
     base = at - lead;
     vecs = RAGGED ? (lead + cols + VEC - 1) / VEC : cols / VEC;
     d = cols;
+    end = row + 1 == rows;
   }
-  // The row's own elements [lo, hi) of its vector c.
+  // Whether vector c may hold other rows' elements; the row's own ones of it are
+  // [lo, hi).
+  __device__ __forceinline__ bool part(int c) const {
+    return RAGGED && (c == 0 || c == vecs - 1);
+  }
   __device__ __forceinline__ int lo(int c) const { return RAGGED && c == 0 ? lead : 0; }
   __device__ __forceinline__ int hi(int c) const {
     return RAGGED ? min(VEC, lead + d - c * VEC) : VEC;
   }
-  // Vector c of a matrix of `total` elements; own() then masks it (apart, so
-  // that all of a row's loads are on their way before the first is used).
+  // Vector c of a matrix; own() then masks it (apart, so that all of a row's
+  // loads are on their way before the first is used).
   template <typename E>
-  __device__ __forceinline__ typename RowVec<E, VEC>::raw load(const void* m, int c,
-                                                               size_t total) const {
-    const size_t at = base + static_cast<size_t>(c) * VEC;
-    const E* p = static_cast<const E*>(m) + at;
-    if (RAGGED && at + VEC > total) return load_part<E, VEC>(p, 0, static_cast<int>(total - at));
+  __device__ __forceinline__ typename RowVec<E, VEC>::raw load(const void* m, int c) const {
+    const E* p = static_cast<const E*>(m) + base + static_cast<size_t>(c) * VEC;
+    if (RAGGED && end && c == vecs - 1) return load_part<E, VEC>(p, lo(c), hi(c));
     return *reinterpret_cast<const typename RowVec<E, VEC>::raw*>(p);
   }
   template <typename E>
   __device__ __forceinline__ void own(typename RowVec<E, VEC>::raw& v, int c) const {
     if constexpr (RAGGED)
-      if (lo(c) > 0 || hi(c) < VEC) v = mask_part<E, VEC>(v, lo(c), hi(c));
+      if (part(c)) v = mask_part<E, VEC>(v, lo(c), hi(c));
   }
   template <typename E>
   __device__ __forceinline__ void store(void* m, int c,
                                         const typename RowVec<E, VEC>::raw& v) const {
     E* p = static_cast<E*>(m) + base + static_cast<size_t>(c) * VEC;
-    if (RAGGED && (lo(c) > 0 || hi(c) < VEC))
+    if (part(c))
       store_part<E, VEC>(p, v, lo(c), hi(c));
     else
       *reinterpret_cast<typename RowVec<E, VEC>::raw*>(p) = v;
@@ -417,7 +421,7 @@ constexpr int kRowThreads = 512;  // of a block that walks a row in two passes
 // KiB of loads in flight (the norm with a residual has two streams, and the
 // weight, per thread).
 __host__ __device__ constexpr int row_regs(int mode, int nv) {
-  return nv == 1 ? 40 : mode == kRowQuant ? 64 : mode == kRowNorm ? 96 : 128;
+  return nv == 1 ? 40 : mode == kRowQuant ? 64 : mode == kRowNorm ? 112 : 128;
 }
 __host__ __device__ constexpr int row_threads_per_sm(int mode, int nv) {
   return 65536 / row_regs(mode, nv);
@@ -448,7 +452,7 @@ __global__ void __maxnreg__(row_regs(MODE, NV)) row_quant_kernel(const RowArgs P
   const long long stride = static_cast<long long>(gridDim.x) * blockDim.y;
   raw w[MODE != kRowQuant ? NV : 1];
   auto load_weight = [&](long long row) {
-    const RowSpan<VEC, RAGGED> span(row, P.d);
+    const RowSpan<VEC, RAGGED> span(row, P.d, P.rows);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
@@ -456,22 +460,21 @@ __global__ void __maxnreg__(row_regs(MODE, NV)) row_quant_kernel(const RowArgs P
     }
   };
   if constexpr (kHoldWeight) load_weight(first);
-  const size_t total = static_cast<size_t>(P.rows) * P.d;
   int buf = 0;
   raw x[NV], t[MODE == kRowNormAdd ? NV : 1];
   auto load_row = [&](long long row) {
-    const RowSpan<VEC, RAGGED> span(row, P.d);
+    const RowSpan<VEC, RAGGED> span(row, P.d, P.rows);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      x[i] = c < span.vecs ? span.template load<E>(P.x, c, total) : RV::zero();
+      x[i] = c < span.vecs ? span.template load<E>(P.x, c) : RV::zero();
       if constexpr (MODE == kRowNormAdd)
-        t[i] = c < span.vecs ? span.template load<E>(P.residual, c, total) : RV::zero();
+        t[i] = c < span.vecs ? span.template load<E>(P.residual, c) : RV::zero();
     }
   };
   if (kAhead && first < P.rows) load_row(first);
   for (long long row = first; row < P.rows; row += stride) {
-    const RowSpan<VEC, RAGGED> span(row, P.d);
+    const RowSpan<VEC, RAGGED> span(row, P.d, P.rows);
     if (!kAhead) load_row(row);
     raw h[NV];
 #pragma unroll
@@ -505,8 +508,8 @@ __global__ void __maxnreg__(row_regs(MODE, NV)) row_quant_kernel(const RowArgs P
 #pragma unroll
           for (int e = 0; e < VEC; ++e) u[e] = 0.f;
         }
-        store_codes<VEC>(P.q + span.base + static_cast<size_t>(c) * VEC, u, inv, span.lo(c),
-                         span.hi(c));
+        store_codes<VEC>(P.q + span.base + static_cast<size_t>(c) * VEC, u, inv, span.part(c),
+                         span.lo(c), span.hi(c));
       }
     }
   }
@@ -522,10 +525,9 @@ __global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowAr
   grid_dependency_wait();
   grid_dependency_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const size_t total = static_cast<size_t>(P.rows) * P.d;
   int buf = 0;
   for (long long row = blockIdx.x; row < P.rows; row += gridDim.x) {
-    const RowSpan<VEC, RAGGED> span(row, P.d);
+    const RowSpan<VEC, RAGGED> span(row, P.d, P.rows);
     auto weight = [&](int c) {
       if constexpr (MODE == kRowQuant)
         return RV::zero();
@@ -536,9 +538,9 @@ __global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowAr
     float top1 = 0.f, sq;
     uint32_t top;
     for (int c = threadIdx.x; c < span.vecs; c += blockDim.x) {
-      raw h = span.template load<E>(P.x, c, total);
+      raw h = span.template load<E>(P.x, c);
       if constexpr (MODE == kRowNormAdd)
-        h = row_h<E, VEC, MODE>(h, span.template load<E>(P.residual, c, total));
+        h = row_h<E, VEC, MODE>(h, span.template load<E>(P.residual, c));
       span.template own<E>(h, c);
       if constexpr (MODE == kRowNormAdd) span.template store<E>(P.h_out, c, h);
       row_stats<E, VEC, MODE>(h, weight(c), sq2, top1);
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowAr
     const float inv = row_inv<MODE>(sq, top);
     if (threadIdx.x == 0) P.scale[row] = row_scale<MODE>(sq, top, inv, P.d, P.eps);
     for (int c = threadIdx.x; c < span.vecs; c += blockDim.x) {
-      raw h = span.template load<E>(MODE == kRowNormAdd ? P.h_out : P.x, c, total);
+      raw h = span.template load<E>(MODE == kRowNormAdd ? P.h_out : P.x, c);
       span.template own<E>(h, c);
       float u[VEC];
       row_u<E, VEC, MODE>(h, weight(c), u);
@@ -557,8 +559,8 @@ __global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowAr
         for (int e = 0; e < VEC; ++e) u[e] = 0.f;
       }
       if (DORA_BOUNDS_OK(c * VEC + span.hi(c) - span.lead <= P.d))
-        store_codes<VEC>(P.q + span.base + static_cast<size_t>(c) * VEC, u, inv, span.lo(c),
-                         span.hi(c));
+        store_codes<VEC>(P.q + span.base + static_cast<size_t>(c) * VEC, u, inv, span.part(c),
+                         span.lo(c), span.hi(c));
     }
   }
 }
