@@ -17,6 +17,10 @@ step, relative):
     term), the last operation once (u of y, or half a bf16 step, 2^-8).
   * h = x + residual: one rounding to the dtype.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -421,6 +425,129 @@ def test_streams_and_graphs(T):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(ref2, out))
+    assert dora.dora_get_device_status() == 0
+
+
+# A fresh process whose first calls happen inside a stream capture: the one-time
+# setup of the kernels then runs during the capture.
+_FIRST_CALL_IN_CAPTURE = r"""
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+import dora_adapter_factored_b200 as dora
+g = torch.Generator().manual_seed(5)
+w = torch.ones(512, device="cuda").bfloat16()
+wq = torch.randint(-127, 128, (384, 512), generator=g).to(torch.int8).cuda()
+sw = torch.rand(384, generator=g).cuda()
+outs = []
+for T in (3, 40, 300):
+    x = torch.randn(T, 512, generator=g).bfloat16().cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, s, h = dora.dora_rmsnorm_quant(x, w, 1e-6, residual=x)
+        y = dora.dora_linear_i8(q, s, wq, sw)
+        z = dora.dora_dequantize_rows(*dora.dora_quantize_rows(y))
+    graph.replay()
+    torch.cuda.synchronize()
+    outs.append((x, q, s, h, y, z))
+for x, *got in outs:
+    q, s, h = dora.dora_rmsnorm_quant(x, w, 1e-6, residual=x)
+    y = dora.dora_linear_i8(q, s, wq, sw)
+    for a, b in zip(got, (q, s, h, y, dora.dora_dequantize_rows(*dora.dora_quantize_rows(y)))):
+        assert torch.equal(a, b)
+assert dora.dora_get_device_status() == 0
+print("OK")
+"""
+
+
+def _child(code, *args):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code, root, *args], capture_output=True, text=True,
+                         timeout=600)
+    assert res.returncode == 0 and "OK" in res.stdout, res.stdout + res.stderr
+
+
+def test_first_calls_inside_a_capture():
+    _child(_FIRST_CALL_IN_CAPTURE)
+
+
+# The debug build on odd shapes: bounds-checked stores, the release build's bits.
+_DEBUG_BUILD = r"""
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+import dora_adapter_factored_b200 as dora
+from dora_adapter_factored_b200 import build
+dora.load_library(build.library_path(debug=sys.argv[2] == "debug"))
+g = torch.Generator().manual_seed(7)
+out = []
+for T, d, d_out in ((1, 7, 5), (3, 1003, 130), (9, 264, 1001), (40, 520, 264), (140, 1001, 77),
+                    (300, 4104, 520), (600, 144, 300), (2, 40000, 9)):
+    for dt in (torch.bfloat16, torch.float32):
+        x = torch.randn(T, d, generator=g).to(dt).cuda()
+        w = torch.randn(d, generator=g).to(dt).cuda()
+        q, s, h = dora.dora_rmsnorm_quant(x, w, 1e-6, residual=x)
+        q2, s2 = dora.dora_quantize_rows(h)
+        wq = torch.randint(-128, 128, (d_out, d), generator=g).to(torch.int8).cuda()
+        sw = torch.rand(d_out, generator=g).cuda()
+        y = dora.dora_linear_i8(q, s, wq, sw, bias=sw, dtype=dt)
+        out += [q, s, h, q2, s2, y, dora.dora_dequantize_rows(q, s, dt)]
+torch.cuda.synchronize()
+assert dora.dora_get_device_status() == 0
+torch.save([t.cpu() for t in out], sys.argv[3])
+print("OK")
+"""
+
+
+def test_debug_build_gives_the_same_bits(built_library, built_debug_library, tmp_path):
+    for kind in ("debug", "release"):
+        _child(_DEBUG_BUILD, kind, str(tmp_path / kind))
+    a, b = (torch.load(tmp_path / kind) for kind in ("debug", "release"))
+    assert len(a) == len(b) and all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_linear_gives_up_on_a_wait_that_runs_out():
+    """With a limit of 1 ns the pipelines' waits run out: the status says so, the
+    context stays usable, and the next call is right."""
+    wq, sw = _codes(1024, 4096, 1), _scales(1024, 1)
+    xq, sx = _codes(600, 4096, 2), _scales(600, 2)
+    for T in (40, 600):
+        ref = dora.dora_linear_i8(xq[:T], sx[:T], wq, sw)
+        assert dora.dora_get_device_status() == 0
+        dora.dora_set_wait_timeout_ns(1)
+        try:
+            dora.dora_linear_i8(xq[:T], sx[:T], wq, sw)
+            status = dora.dora_get_device_status()
+        finally:
+            dora.dora_set_wait_timeout_ns(0)
+        assert status in (0, 5)
+        got = dora.dora_linear_i8(xq[:T], sx[:T], wq, sw)
+        assert dora.dora_get_device_status() == 0 and torch.equal(got, ref)
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements: the last rows are where they belong."""
+    rows, cols = 131200, 16392
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    last = _rand(3, cols, "bf16", 1)
+    x[-3:] = last
+    q, scale = dora.dora_quantize_rows(x)
+    _check_quant(last, q[-3:], scale[-3:], "last rows")
+    assert not scale[:-3].any() and not q[:-3:1000].any()
+    w = torch.ones(cols, device="cuda", dtype=torch.bfloat16)
+    q, scale, h = dora.dora_rmsnorm_quant(x, w, EPS, residual=x, h_out=x, q=q, scale=scale)
+    _check_norm(last, w, last, q[-3:], scale[-3:], h[-3:], "norm of last rows")
+    del x, h
+    v = dora.dora_dequantize_rows(q, scale)
+    want = (q[-3:].cpu().float() * scale[-3:].cpu()[:, None]).bfloat16()
+    assert torch.equal(v[-3:].cpu(), want)
+    del v, q, scale
+    T, d_out, d_in = 70000, 32776, 48
+    xq, sx = _codes(T, d_in, 3), _scales(T, 3)
+    wq, sw = _codes(d_out, d_in, 4), _scales(d_out, 4)
+    y = dora.dora_linear_i8(xq, sx, wq, sw)
+    for rows in (slice(0, 2), slice(T // 2, T // 2 + 2), slice(T - 2, T)):
+        _check_linear(y[rows], xq[rows], sx[rows], wq, sw, None, f"rows {rows}")
     assert dora.dora_get_device_status() == 0
 
 
