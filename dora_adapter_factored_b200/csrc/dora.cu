@@ -2118,8 +2118,10 @@ dora_status_t run_rows(const RowArgs& P, dora_dtype_t dt, int mode, dora_stream_
 template <typename E, int VEC>
 void launch_dequant(const int8_t* q, const float* scale, int64_t rows, int cols, E* x,
                     cudaStream_t cs) {
+  // Several waves of short blocks: 62.6 us at [25600, 5120], against 67.4 where
+  // the blocks are one wave that walks on.
   const StreamGrid g = stream_grid(rows, static_cast<int>(ceil_div_ll(cols, VEC)),
-                                   kDequantRowUnroll, 4 * kStreamSlots);
+                                   kDequantRowUnroll, 16 * kStreamSlots);
   launch_stream(dequant_rows_kernel<E, VEC>, dim3(g.gx, std::min(g.gy, 65535)),
                 dim3(kStreamThreads), 0, cs, q, scale, static_cast<long long>(rows), cols, x,
                 g.bx);

@@ -339,8 +339,9 @@ dora_status_t dora_merge_weight(const void *W0, const void *A, const void *B, co
 /* Rows of x [rows, cols] (dtype `dt`) to codes q [rows, cols] and scale
  * [rows] fp32.  Outputs must not overlap x or each other.  rows == 0 launches
  * nothing.  rows, cols <= 2^30.  One launch; x is read once where a row fits
- * the registers of a block (16384 bf16 or 8192 fp32 elements; 8192 where rows
- * are not 16-byte aligned), else twice. */
+ * the registers of a block (32768 bf16 or 16384 fp32 elements; 16384 where x
+ * or q is not aligned), else twice.  Fastest where x is 16-byte aligned and q
+ * 8-byte (4-byte for fp32); row lengths need no alignment. */
 dora_status_t dora_quantize_rows(const void *x, dora_dtype_t dt, int64_t rows, int64_t cols,
                                  int8_t *q, float *scale, dora_stream_t stream);
 
@@ -360,7 +361,9 @@ dora_status_t dora_dequantize_rows(const int8_t *q, const float *scale, dora_dty
  * `dt`; q [T, d]; scale [T] fp32; eps > 0 and finite.  Sums and products are
  * fp32: a row whose sum of squares, or whose h weight, passes fp32's range
  * counts as not finite.  h_out may equal x or residual (element for element);
- * no other overlap.  T == 0 launches nothing.  T, d <= 2^30.  One launch. */
+ * no other overlap.  T == 0 launches nothing.  T, d <= 2^30.  One launch; x
+ * (and the residual) are read once up to 16384 bf16 or 8192 fp32 elements a
+ * row.  Alignment as above, and weight 16-byte aligned. */
 dora_status_t dora_rmsnorm_quant(const void *x, const void *residual, const void *weight,
                                  float eps, dora_dtype_t dt, int64_t T, int64_t d, void *h_out,
                                  int8_t *q, float *scale, dora_stream_t stream);
@@ -376,7 +379,12 @@ dora_status_t dora_rmsnorm_quant(const void *x, const void *residual, const void
  * (DORA_F32 or DORA_BF16).  d_in <= DORA_MAX_I8_K, T <= 2^23, d_out <= 2^30
  * (DORA_ERR_UNSUPPORTED otherwise).  y must not overlap an input.  T == 0
  * launches nothing.  Workspace: dora_linear_i8_workspace_size() bytes, 256-byte
- * aligned, contents undefined on entry and exit (0 bytes: ws may be NULL). */
+ * aligned, contents undefined on entry and exit (0 bytes: ws may be NULL; it
+ * holds copies of rows whose length is not a multiple of 16, and belongs to
+ * the call until it has run: two calls that overlap, or two captured graphs
+ * that may, need one each).  With d_in a multiple of 16, xq and wq should be
+ * 16-byte aligned: otherwise the call is computed with dot products, right
+ * but far slower for more than a few tokens.  Up to two launches. */
 #define DORA_MAX_I8_K 131071
 size_t dora_linear_i8_workspace_size(int64_t T, int64_t d_out, int64_t d_in);
 dora_status_t dora_linear_i8(const int8_t *xq, const float *x_scale, const int8_t *wq,
