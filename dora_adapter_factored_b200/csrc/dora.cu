@@ -2040,10 +2040,15 @@ void launch_rows_nv(const RowArgs& P, long long nvec, int sms, cudaStream_t cs) 
     prefer_l1(reinterpret_cast<const void*>(kernel), kRowMaxCtasPerSm);
     launch_pdl(kernel, blocks, dim3(threads, by), 0, cs, P);
   };
-  if (fits)
-    go(row_quant_kernel<E, VEC, NV, MODE, RAGGED>);
-  else
-    go(row_quant_long_kernel<E, VEC, MODE, RAGGED>);
+  if constexpr (NV > 1)  // rows of one vector per lane always fit
+    if (!fits) return go(row_quant_long_kernel<E, VEC, MODE, RAGGED>);
+  if constexpr (MODE != kRowQuant) {
+    go(row_quant_kernel<E, VEC, NV, MODE, RAGGED, true>);
+  } else {
+    if constexpr (NV > 1)
+      if (per_sm == 1) return go(row_quant_kernel<E, VEC, NV, MODE, RAGGED, true>);
+    go(row_quant_kernel<E, VEC, NV, MODE, RAGGED, false>);
+  }
 }
 
 template <typename E, int VEC, int MODE, bool RAGGED>

@@ -246,14 +246,14 @@ template <int VEC, bool RAGGED>
 struct RowSpan {
   size_t base;
   int lead, vecs, d;
-  bool end;  // the matrix's last row: its last vector may reach past the matrix
+  bool end;  // the last vector reaches past the matrix
   __device__ __forceinline__ RowSpan(long long row, int cols, long long rows) {
     const size_t at = static_cast<size_t>(row) * cols;
     lead = RAGGED ? static_cast<int>(at % VEC) : 0;
     base = at - lead;
     vecs = RAGGED ? (lead + cols + VEC - 1) / VEC : cols / VEC;
     d = cols;
-    end = row + 1 == rows;
+    end = RAGGED && base + static_cast<size_t>(vecs) * VEC > static_cast<size_t>(rows) * cols;
   }
   // Whether vector c may hold other rows' elements; the row's own ones of it are
   // [lo, hi).
@@ -408,9 +408,15 @@ __device__ __forceinline__ float row_scale(float sq, uint32_t top, float inv, in
 // Rows of up to NV vectors per thread.  A group of blockDim.x threads (a
 // multiple of 32) takes a row; blockDim.y groups share a block only where a
 // group is one warp.  Blocks walk the rows with the grid's stride, which has
-// to be the blocks that are resident at once (more would run as a second
-// wave: 103 instead of 71 us at [25600, 5120]); the register bound keeps the
+// to be the blocks that are resident at once (one more per SM runs as a second
+// wave: 81 instead of 62 us at [25600, 5120]); the register bound keeps the
 // two in step.
+// AHEAD: the next row's loads are on their way while a row is reduced and
+// stored, which the norm needs (93 instead of 88 % of the HBM rate at [8192,
+// 8192]) and rows of which an SM holds one block (24 instead of 30 us for
+// [2048, 14336] fp32); several blocks of rows that are only quantised overlap by
+// themselves, and the registers cost them more (62 against 67 us at [25600,
+// 5120]).
 // NV: 16-byte vectors per thread, 4, or 1 for rows that a warp holds so (short
 // rows need many of them in flight); or elements, where the matrix itself is
 // not aligned.
@@ -431,7 +437,7 @@ __host__ __device__ constexpr int row_max_threads(int mode) {
   return row_threads_per_sm(mode, kRowVecs) >= 1024 ? 1024 : 512;
 }
 
-template <typename E, int VEC, int NV, int MODE, bool RAGGED>
+template <typename E, int VEC, int NV, int MODE, bool RAGGED, bool AHEAD>
 __global__ void __maxnreg__(row_regs(MODE, NV)) row_quant_kernel(const RowArgs P) {
   using RV = RowVec<E, VEC>;
   using raw = typename RV::raw;
@@ -439,11 +445,6 @@ __global__ void __maxnreg__(row_regs(MODE, NV)) row_quant_kernel(const RowArgs P
   // the grid's stride is a multiple of VEC rows where rows are ragged.
   // Element by element there is no room for it, and it is read for each row.
   constexpr bool kHoldWeight = MODE != kRowQuant && VEC > 1;
-  // The next row's loads are on their way while a row is reduced and stored:
-  // 93 instead of 88 % of the HBM rate for the norm at [8192, 8192].  Rows that
-  // are only quantised have twice the threads instead (71 against 75 us at
-  // [25600, 5120]).
-  constexpr bool kAhead = MODE != kRowQuant;
   __shared__ uint2 red[2][32];
   grid_dependency_wait();
   grid_dependency_trigger();
@@ -472,10 +473,10 @@ __global__ void __maxnreg__(row_regs(MODE, NV)) row_quant_kernel(const RowArgs P
         t[i] = c < span.vecs ? span.template load<E>(P.residual, c) : RV::zero();
     }
   };
-  if (kAhead && first < P.rows) load_row(first);
+  if (AHEAD && first < P.rows) load_row(first);
   for (long long row = first; row < P.rows; row += stride) {
     const RowSpan<VEC, RAGGED> span(row, P.d, P.rows);
-    if (!kAhead) load_row(row);
+    if (!AHEAD) load_row(row);
     raw h[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -486,7 +487,7 @@ __global__ void __maxnreg__(row_regs(MODE, NV)) row_quant_kernel(const RowArgs P
         if constexpr (MODE == kRowNormAdd) span.template store<E>(P.h_out, c, h[i]);
       }
     }
-    if (kAhead && row + stride < P.rows) load_row(row + stride);
+    if (AHEAD && row + stride < P.rows) load_row(row + stride);
     if constexpr (MODE != kRowQuant && !kHoldWeight) load_weight(row);
     uint64_t sq2 = 0;
     float top1 = 0.f, sq;
