@@ -2053,8 +2053,7 @@ void launch_rows_nv(const RowArgs& P, long long nvec, int sms, cudaStream_t cs) 
 
 template <typename E, int VEC, int MODE, bool RAGGED>
 void launch_rows(const RowArgs& P, int sms, cudaStream_t cs) {
-  // The most vectors a row can touch.
-  const long long nvec = ceil_div_ll(static_cast<long long>(P.d) + (RAGGED ? VEC - 1 : 0), VEC);
+  const long long nvec = std::max(1, P.d / VEC);  // the most whole ones of a row
   if constexpr (VEC == 1)
     launch_rows_nv<E, VEC, kRowScalars, MODE, RAGGED>(P, nvec, sms, cs);
   else if (nvec <= 32)
