@@ -122,6 +122,29 @@ def test_many_rows(T, d, dt):
     _check_norm(x, w, r, q, scale, h, "norm")
 
 
+@pytest.mark.parametrize("T,d,dt", [(20001, 3, "f32"), (20001, 7, "bf16"), (3001, 129, "f32"),
+                                    (2503, 257, "bf16"), (1300, 1023, "bf16"), (700, 4099, "f32"),
+                                    (650, 8191, "bf16"), (330, 8191, "f32"), (200, 16383, "f32"),
+                                    (310, 16383, "bf16")])
+def test_many_ragged_rows(T, d, dt):
+    """Rows that start anywhere in a vector, more than the grid has blocks: the
+    walked rows start alike, and no row sees its neighbours' elements."""
+    x, r = _rand(T, d, dt, 3), _rand(T, d, dt, 4)
+    w = (1 + 0.2 * _rand(1, d, dt, 5)[0].float()).to(DTYPES[dt]).contiguous()
+    q, scale = dora.dora_quantize_rows(x)
+    _check_quant(x, q, scale, "quantize")
+    q, scale, h = dora.dora_rmsnorm_quant(x, w, EPS)
+    _check_norm(x, w, None, q, scale, h, "norm")
+    alone = (q, scale)
+    q, scale, h = dora.dora_rmsnorm_quant(x, w, EPS, residual=r)
+    _check_norm(x, w, r, q, scale, h, "norm of a sum")
+    # every other row not finite: the rows between them keep their bits
+    x[1::2] = float("nan")
+    q, scale, _ = dora.dora_rmsnorm_quant(x, w, EPS)
+    assert torch.equal(q[::2], alone[0][::2]) and torch.equal(scale[::2], alone[1][::2])
+    assert not q[1::2].any() and torch.isnan(scale[1::2]).all()
+
+
 @pytest.mark.parametrize("d", [1000, 40000])
 def test_alignment_does_not_change_results(d):
     """Views that start off a 16-byte boundary take the element path: the same
@@ -210,6 +233,18 @@ def test_dequantize_rows(T, d, dt):
     out = dora.dora_dequantize_rows(qb, scale, x=xb[1:].view(T, d))
     _intact((xw, xg))
     assert torch.equal(out.nan_to_num(), x.nan_to_num())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(30011, 1401), (300007, 137), (6000001, 7), (20000003, 2)])
+def test_dequantize_more_than_the_grid_at_once(T, d, dt):
+    """Threads that follow their rows from one vector to the next, over vectors
+    of one row, of two and of several."""
+    g = torch.Generator("cuda").manual_seed(d)
+    q = torch.randint(-127, 128, (T, d), dtype=torch.int8, device="cuda", generator=g)
+    scale = torch.rand(T, device="cuda", generator=g) + 0.5
+    want = (q.float() * scale[:, None]).to(DTYPES[dt])
+    assert torch.equal(dora.dora_dequantize_rows(q, scale, DTYPES[dt]), want)
 
 
 def test_weight_held_as_codes_through_norm_and_merge():
