@@ -2180,10 +2180,14 @@ void launch_dot_any(const LinearArgs& P, bool vec, int sms, cudaStream_t cs) {
 // The most tokens the dot-product kernel takes where the tensor cores could.
 constexpr int kDotMaxT = kDotTokens;
 
-int padded_k(int64_t d_in) { return static_cast<int>(align_up(static_cast<size_t>(d_in), 16)); }
+// Bytes of a row of the padded copies of xq and wq, which TMA needs where a row
+// is not a multiple of 16 bytes: whole lines (31.9 us for one token through
+// 14336 x 4097 with multiples of 16, 30.3 so).  Rows that are an odd multiple of
+// 16 bytes are read as they are: a large product of them takes 1.2 to 1.6 times
+// as long as one of whole lines, but copying them first gained 22 % at the most
+// (5431 x 4440 x 6064) and lost 13 % elsewhere (1200 x 25600 x 5104).
+int padded_k(int64_t d_in) { return static_cast<int>(align_up(static_cast<size_t>(d_in), kI8K)); }
 
-// Bytes of the padded copies of xq and wq, which TMA needs where a row is not
-// a multiple of 16 bytes.
 size_t linear_pad_x(int64_t T, int64_t d_in) {
   return align_up(static_cast<size_t>(T) * padded_k(d_in), 256);
 }
