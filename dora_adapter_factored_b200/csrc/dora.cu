@@ -2031,8 +2031,12 @@ void launch_rows_nv(const RowArgs& P, long long nvec, int sms, cudaStream_t cs) 
   const int threads = fits ? static_cast<int>(want) : kRowThreads;
   const int by = fits && threads == 32 ? 8 : 1;  // one-warp rows share a block
   const long long groups = ceil_div_ll(P.rows, by);
-  const int per_sm = std::max(1, (fits ? row_threads_per_sm(MODE, NV) : 2 * kRowThreads) /
-                                     (threads * by));
+  int per_sm = std::max(1, (fits ? row_threads_per_sm(row_regs(MODE, NV)) : 2 * kRowThreads) /
+                               (threads * by));
+  constexpr bool kMayTakeFew = MODE == kRowNorm && sizeof(E) == 4 && NV == kRowVecs;
+  const int per_sm_few = row_threads_per_sm(kRowFewRegs) / (threads * by);
+  const bool few = kMayTakeFew && fits && per_sm_few > per_sm;
+  if (few) per_sm = per_sm_few;
   long long grid = static_cast<long long>(sms) * per_sm;
   if (RAGGED && grid * by % VEC != 0) grid = std::max<long long>(VEC, grid / VEC * VEC);
   const dim3 blocks(static_cast<unsigned>(std::min(groups, grid)));
@@ -2042,6 +2046,8 @@ void launch_rows_nv(const RowArgs& P, long long nvec, int sms, cudaStream_t cs) 
   };
   if constexpr (NV > 1)  // rows of one vector per lane always fit
     if (!fits) return go(row_quant_long_kernel<E, VEC, MODE, RAGGED>);
+  if constexpr (kMayTakeFew)
+    if (few) return go(row_quant_kernel<E, VEC, NV, MODE, RAGGED, true, kRowFewRegs>);
   if constexpr (MODE != kRowQuant) {
     go(row_quant_kernel<E, VEC, NV, MODE, RAGGED, true>);
   } else {
