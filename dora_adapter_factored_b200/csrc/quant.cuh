@@ -499,13 +499,18 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
 }
 
 // Rows longer than the registers hold: two passes over the row, the second
-// from L2 (of h, as this thread stored it, where there is a residual).
+// from L2 (of h, as this thread stored it, where there is a residual), with a
+// few vectors on their way at a time (one by one [4096, 14336] fp32 took 80 us, 147
+// with a residual, against 65 and 131; with the weight's as well they spill, 129
+// and 274).
+constexpr int kRowLongVecs = 4;  // half that of two streams
 template <typename E, int VEC, int MODE, bool RAGGED>
-__global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowArgs P) {
+__global__ void __launch_bounds__(kRowThreads, 2) row_quant_long_kernel(const RowArgs P) {
   using RV = RowVec<E, VEC>;
   using RV1 = RowVec<E, 1>;
   using raw = typename RV::raw;
   using raw1 = typename RV1::raw;
+  constexpr int U = MODE == kRowNormAdd ? kRowLongVecs / 2 : kRowLongVecs;
   __shared__ uint2 red[2][32];
   grid_dependency_wait();
   grid_dependency_trigger();
@@ -525,13 +530,26 @@ __global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowAr
     uint64_t sq2 = 0;
     float top1 = 0.f, sq;
     uint32_t top;
-    for (int c = threadIdx.x; c < span.vecs; c += blockDim.x) {
-      raw h = load_vec<E, VEC>(P.x, at + span.column(c));
-      if constexpr (MODE == kRowNormAdd) {
-        h = row_h<E, VEC, MODE>(h, load_vec<E, VEC>(P.residual, at + span.column(c)));
-        store_vec<E, VEC>(P.h_out, at + span.column(c), h);
+    for (int c0 = threadIdx.x; c0 < span.vecs; c0 += U * blockDim.x) {
+      raw h[U], t[MODE == kRowNormAdd ? U : 1];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int c = c0 + i * blockDim.x;
+        h[i] = c < span.vecs ? load_vec<E, VEC>(P.x, at + span.column(c)) : RV::zero();
+        if constexpr (MODE == kRowNormAdd)
+          t[i] = c < span.vecs ? load_vec<E, VEC>(P.residual, at + span.column(c)) : RV::zero();
       }
-      row_stats<E, VEC, MODE>(h, weight(c), sq2, top1);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int c = c0 + i * blockDim.x;
+        if (c < span.vecs) {
+          if constexpr (MODE == kRowNormAdd) {
+            h[i] = row_h<E, VEC, MODE>(h[i], t[i]);
+            store_vec<E, VEC>(P.h_out, at + span.column(c), h[i]);
+          }
+          row_stats<E, VEC, MODE>(h[i], weight(c), sq2, top1);
+        }
+      }
     }
     raw1 hl = RV1::zero(), wl = RV1::zero();
     if constexpr (RAGGED)
@@ -548,10 +566,21 @@ __global__ void __launch_bounds__(kRowThreads) row_quant_long_kernel(const RowAr
     buf ^= 1;
     const float inv = row_inv<MODE>(sq, top);
     if (threadIdx.x == 0) P.scale[row] = row_scale<MODE>(sq, top, inv, P.d, P.eps);
-    for (int c = threadIdx.x; c < span.vecs; c += blockDim.x) {
-      const raw h = load_vec<E, VEC>(MODE == kRowNormAdd ? P.h_out : P.x, at + span.column(c));
-      if (DORA_BOUNDS_OK(span.column(c) + VEC <= static_cast<size_t>(P.d)))
-        row_codes<E, VEC, MODE>(h, weight(c), inv, P.q + at + span.column(c));
+    for (int c0 = threadIdx.x; c0 < span.vecs; c0 += U * blockDim.x) {
+      raw h[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int c = c0 + i * blockDim.x;
+        h[i] = c < span.vecs ? load_vec<E, VEC>(MODE == kRowNormAdd ? P.h_out : P.x,
+                                                at + span.column(c))
+                             : RV::zero();
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int c = c0 + i * blockDim.x;
+        if (c < span.vecs && DORA_BOUNDS_OK(span.column(c) + VEC <= static_cast<size_t>(P.d)))
+          row_codes<E, VEC, MODE>(h[i], weight(c), inv, P.q + at + span.column(c));
+      }
     }
     if constexpr (RAGGED)
       if (loose >= 0 && DORA_BOUNDS_OK(loose < P.d))
