@@ -438,7 +438,6 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
     if constexpr (RAGGED)
       if (loose >= 0) wl = load_vec<E, 1>(P.weight, loose);
   };
-  if constexpr (kHoldWeight) load_weight();
   int buf = 0;
   raw x[NV], t[MODE == kRowNormAdd ? NV : 1];
   raw1 xl = RV1::zero(), tl = RV1::zero();
@@ -457,7 +456,8 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
         if constexpr (MODE == kRowNormAdd) tl = load_vec<E, 1>(P.residual, at + loose);
       }
   };
-  if (AHEAD && first < P.rows) load_row(first);
+  if (AHEAD && first < P.rows) load_row(first);  // before the weight's are waited for
+  if constexpr (kHoldWeight) load_weight();
   for (long long row = first; row < P.rows; row += stride) {
     const size_t at = static_cast<size_t>(row) * P.d;
     if (!AHEAD) load_row(row);
