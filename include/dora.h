@@ -327,8 +327,10 @@ dora_status_t dora_merge_weight(const void *W0, const void *A, const void *B, co
  * A row v of values is held as  scale = max_j |v_j| / 127  and
  * q_j = round(v_j / scale), half to even, in [-127, 127]; v_j is then
  * approximately q_j scale, to half a step.  The quotient is formed as
- * v_j (127 / max|v|) in fp32, so a value within about 2^-23 of its size from
- * the middle between two codes may take either.
+ * v_j (127 / max|v|), with the factor rounded up to fp32: rows of bf16 values get
+ * exactly these codes; of fp32 values, and behind the norm, one that is less
+ * than 2^-23 of its size short of the middle between two codes, or on it, may
+ * take the larger.
  *   - A row whose step max|v| / 127 is below the smallest normal fp32
  *     (2^-126), an all-zero row among them: codes 0, scale 0.
  *   - A row with an infinity or a NaN: codes 0, scale NaN, so that the outputs
