@@ -2029,7 +2029,7 @@ void launch_rows_nv(const RowArgs& P, long long nvec, int sms, cudaStream_t cs) 
   const long long want = ceil_div_ll(ceil_div_ll(nvec, NV), 32) * 32;
   const bool fits = want <= row_max_threads(MODE);
   const int threads = fits ? static_cast<int>(want) : kRowThreads;
-  const int by = fits && threads == 32 ? 8 : 1;  // one-warp rows share a block
+  const int by = fits && threads == 32 ? kRowGroups : 1;  // one-warp rows share a block
   const long long groups = ceil_div_ll(P.rows, by);
   int per_sm = std::max(1, (fits ? row_threads_per_sm(row_regs(MODE, NV)) : 2 * kRowThreads) /
                                (threads * by));

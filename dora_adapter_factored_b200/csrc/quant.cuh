@@ -7,17 +7,19 @@
 //           the dtype                                 (dora_rmsnorm_quant)
 //   scale = max_j |v_j| / 127,   q_j = rint(v_j / scale)
 //
-// The codes do not need the rms: it is a common factor of the row, so with
-// u_j = h_j w_j and a = max |u_j|,  q_j = rint(u_j (127 / a))  and
-// scale = (a / 127) / rms.  The row's sum of squares and its maximum are
-// therefore reduced together, in one pass and with one block barrier, and the
-// row stays in registers in between: x (and the residual) are read once, h
-// and the codes written once.
+// The codes do not need the rms (but where it decides whether there is a step at
+// all): it is a common factor of the row, so with u_j = h_j w_j and a = max |u_j|,
+// q_j = rint(u_j (127 / a))  and  scale = (a / 127) / rms.  The row's sum of
+// squares and its maximum are therefore reduced together, in one pass and with
+// one block barrier, and the row stays in registers in between: x (and the
+// residual) are read once, h and the codes written once.
 //
 // Sums, maxima and products are fp32; h is rounded to the dtype because it is
 // stored and read again by the next layer, and the norm is of that stored
 // value.  A sum of squares beyond fp32's range counts as not finite.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "compose.cuh"
@@ -73,7 +75,7 @@ struct RowArgs {
   void* h_out;
   int8_t* q;
   float* scale;
-  long long rows;
+  long long rows;  // at most 2^30, as d
   int d;
   float eps;
 };
@@ -344,38 +346,178 @@ __device__ __forceinline__ void row_reduce(uint64_t sq2, float top1, int warps, 
   top = __reduce_max_sync(0xffffffffu, top);
 }
 
-// Factor of the codes from the row's maximum (and, where it is a norm, its sum
-// of squares, which has to be finite): 0 for a row that is not finite and for
-// one whose step max / 127 would not be a normal number.  127 / max is rounded
-// up: a value of half the maximum, code 63.5 exactly, then never falls short of
-// the half that goes to the even 64 (rounded to nearest, it did for 66 of the 128
+// Factor of the codes from the row's maximum: 127 / max rounded up, so that a
+// value of half the maximum, code 63.5 exactly, never falls short of the half
+// that goes to the even 64 (rounded to nearest, it did for 66 of the 128
 // mantissas of a bf16 maximum).  Every other code of a row of 8-bit mantissas is
 // at least 1/510 of its power of two from a half, against 2^-23 that the factor
 // is off, or its 127 / max is exact: such rows get the codes of the definition.
-template <int MODE>
-__device__ __forceinline__ float row_inv(float sq, uint32_t top) {
-  bool live = top < kInfBits && __uint_as_float(top) >= kCodeMax * kMinNormal;
-  if constexpr (MODE != kRowQuant) live = live && __float_as_uint(sq) < kInfBits;
-  // (the nearest, or the next where the sign of the exact residual says that it
-  // is below; the rounded-up division is a call, whose registers cost the norm at
-  // [8192, 8192] bf16 47 instead of 38 us)
-  const float a = __uint_as_float(top), inv = __fdiv_rn(kCodeMax, a);
-  const uint32_t up = __fmaf_rn(a, inv, -kCodeMax) < 0.f ? 1u : 0u;
-  return live ? __uint_as_float(__float_as_uint(inv) + up) : 0.f;
+// (The nearest quotient, or the next where the sign of the exact residual says
+// that it is below; the rounded-up division is a call, whose registers cost the
+// norm at [8192, 8192] bf16 47 instead of 38 us.)
+__device__ __forceinline__ float code_factor(float top) {
+  const float inv = __fdiv_rn(kCodeMax, top);
+  const uint32_t up = __fmaf_rn(top, inv, -kCodeMax) < 0.f ? 1u : 0u;
+  return __uint_as_float(__float_as_uint(inv) + up);
 }
 
-// The row's scale, which no thread but the one that stores it waits for: NaN
-// for a row that is not finite, 0 where there is no step.
-template <int MODE>
-__device__ __forceinline__ float row_scale(float sq, uint32_t top, float inv, int d, float eps) {
-  const bool finite =
-      top < kInfBits && (MODE == kRowQuant || __float_as_uint(sq) < kInfBits);
-  if (!finite) return __uint_as_float(0x7fc00000u);
-  if (inv == 0.f) return 0.f;
-  const float step = __fdiv_rn(__uint_as_float(top), kCodeMax);
-  if constexpr (MODE == kRowQuant) return step;
+// What a row that is only quantised is held with, from its maximum: factor 0 for
+// one that is not finite and for one whose step max / 127 would not be a normal
+// number, scale NaN and 0 there.
+__device__ __forceinline__ float quant_inv(uint32_t top) {
+  const bool live = top < kInfBits && __uint_as_float(top) >= kCodeMax * kMinNormal;
+  return live ? code_factor(__uint_as_float(top)) : 0.f;
+}
+__device__ __forceinline__ float quant_scale(uint32_t top, float inv) {
+  if (top >= kInfBits) return __uint_as_float(0x7fc00000u);
+  return inv == 0.f ? 0.f : __fdiv_rn(__uint_as_float(top), kCodeMax);
+}
+
+// Behind the norm the step is max|h w| / 127 / rms.  For an ordinary row
+// (sq + eps < 2^100 keeps 1 / rms in 2^-50 .. 2^75) it is a normal number whatever
+// the rms, which therefore only the thread that stores the scale forms.
+__device__ __forceinline__ bool norm_row_ordinary(float sq, uint32_t top, float eps) {
+  return __fadd_rn(sq, eps) < 0x1p100f && __uint_as_float(top) >= 0x1p-50f &&
+         __uint_as_float(top) <= 0x1p40f;
+}
+// Of the others, one that is not finite is held as codes 0 with scale NaN and one
+// of zeros as codes 0 with scale 0, which are all there are in practice.  The rest
+// need their rms: their scale is kRowAgain until they are taken again, behind the
+// block's last row.  (Products up to 2^-150 are 0 too, but only a 1 / rms above
+// 2^30 gives those a step.)
+constexpr float kRowAgain = -1.f;
+__device__ __forceinline__ bool norm_row_finite(float sq, uint32_t top) {
+  return top < kInfBits && __float_as_uint(sq) < kInfBits;
+}
+__device__ __forceinline__ bool norm_row_again(float sq, uint32_t top, float eps) {
+  return norm_row_finite(sq, top) && (top != 0u || eps < 0x1p-60f);
+}
+__device__ __forceinline__ float norm_rstd(float sq, int d, float eps) {
   const float mean = __fdiv_rn(sq, static_cast<float>(d));
-  return __fmul_rn(step, __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(mean, eps))));
+  return __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(mean, eps)));
+}
+__device__ __forceinline__ float norm_scale(float sq, uint32_t top, int d, float eps) {
+  return __fmul_rn(__fdiv_rn(__uint_as_float(top), kCodeMax), norm_rstd(sq, d, eps));
+}
+
+// max|h w| may be too small for its quotient by 127, or h w for fp32, where
+// 1 / rms (up to 2^75 for the smallest eps) brings the step back into range: such
+// a row is computed with h lifted by 2^96.  That is exact, since 1 / rms is then
+// above 1/2 and |h| at most 2 sqrt(d), and the row's maximum becomes at most
+// 2^-23.
+constexpr float kRowLift = 0x1p96f;
+__device__ __forceinline__ bool norm_row_lifts(float sq, uint32_t top, int d, float eps) {
+  const float a = __uint_as_float(top);
+  if (a >= kCodeMax * kMinNormal) return false;
+  // (products below 2^-150 are 0; a little beyond the bound costs only time)
+  return __fmul_rn(__fadd_rn(a, 0x1p-149f), norm_rstd(sq, d, eps)) >= 126.f * kMinNormal;
+}
+
+// Indices of the thread and the block, read here and not kept from an earlier use.
+struct FreshIndex {
+  int tid_x, tid_y, cta, ctas, threads, groups;
+  __device__ __forceinline__ FreshIndex() {
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid_x));
+    asm volatile("mov.u32 %0, %%tid.y;" : "=r"(tid_y));
+    asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta));
+    asm volatile("mov.u32 %0, %%nctaid.x;" : "=r"(ctas));
+    asm volatile("mov.u32 %0, %%ntid.x;" : "=r"(threads));
+    asm volatile("mov.u32 %0, %%ntid.y;" : "=r"(groups));
+  }
+};
+
+// A row that needs its rms, again from memory, element by element; the same way in
+// all its threads, which have met at a barrier since h was stored.  Behind the
+// loop over the rows, small, and with nothing kept for it there: in the loop, by
+// vectors, its registers cost the ragged norm with a residual ([8192, 8191] bf16)
+// 94 instead of 76 us; so 78, and the norm of [4096, 14336] fp32 133 instead of 131.
+template <typename E, int MODE>
+__device__ __forceinline__ void norm_row_from_memory(const RowArgs& P, int row, int tid,
+                                                     int threads, uint2 (&red)[2][32],
+                                                     int& buf) {
+  const int d = P.d;
+  const E* h = static_cast<const E*>(MODE == kRowNormAdd ? P.h_out : P.x) +
+               static_cast<size_t>(row) * d;
+  const E* w = static_cast<const E*>(P.weight);
+  float lift = 1.f;
+  auto stats = [&](float& sq, uint32_t& top) {
+    float s = 0.f, m = 0.f;
+#pragma unroll 1
+    for (int c = tid; c < d; c += threads) {
+      const float v = static_cast<float>(h[c]);
+      s = __fmaf_rn(v, v, s);
+      m = fmaxf(m, fabsf(__fmul_rn(__fmul_rn(v, lift), static_cast<float>(w[c]))));
+    }
+    row_reduce(pair_f32(s, 0.f), m, threads >> 5, tid >> 5, tid & 31, red[buf], sq, top);
+    buf ^= 1;
+  };
+  float sq;
+  uint32_t top;
+  stats(sq, top);
+  if (norm_row_lifts(sq, top, d, P.eps)) {
+    float unused;
+    lift = kRowLift;
+    stats(unused, top);
+  }
+  float inv = 0.f, scale = 0.f;
+  if (__uint_as_float(top) >= kCodeMax * kMinNormal) {
+    scale = __fmul_rn(norm_scale(sq, top, d, P.eps), lift == 1.f ? 1.f : 1.f / kRowLift);
+    if (scale >= kMinNormal)
+      inv = code_factor(__uint_as_float(top));
+    else
+      scale = 0.f;
+  }
+  if (tid == 0) P.scale[row] = scale;
+#pragma unroll 1
+  for (int c = tid; c < d; c += threads) {
+    const float u[1] = {
+        __fmul_rn(__fmul_rn(static_cast<float>(h[c]), lift), static_cast<float>(w[c]))};
+    if (DORA_BOUNDS_OK(row < P.rows))
+      store_codes<1>(P.q + static_cast<size_t>(row) * d + c, u, inv);
+  }
+}
+
+// The factor of a row: 0 where its codes are 0 or are to be taken again.
+template <int MODE>
+__device__ __forceinline__ float row_inv(float sq, uint32_t top, float eps) {
+  if constexpr (MODE == kRowQuant) return quant_inv(top);
+  return norm_row_ordinary(sq, top, eps) ? code_factor(__uint_as_float(top)) : 0.f;
+}
+// The row's scale, which no thread but the one that stores it waits for.  `again`
+// (shared by the row's threads) is set where the row is to be taken again.
+template <int MODE>
+__device__ __forceinline__ float row_scale(float sq, uint32_t top, float inv, int d, float eps,
+                                           int& again) {
+  if constexpr (MODE == kRowQuant) return quant_scale(top, inv);
+  if (inv != 0.f) return norm_scale(sq, top, d, eps);
+  if (!norm_row_finite(sq, top)) return __uint_as_float(0x7fc00000u);
+  if (!norm_row_again(sq, top, eps)) return 0.f;
+  again = 1;
+  return kRowAgain;
+}
+
+// Behind the loop over a block's rows: those that were left, if any was (`again`:
+// one flag per block, at a fixed address; by row group its address had to live
+// through the loop, with the registers and the time named above).
+template <typename E, int MODE>
+__device__ __forceinline__ void norm_rows_again(const RowArgs& P, const int& again,
+                                                uint2 (&red)[2][32]) {
+  const FreshIndex at;
+  auto sync_row = [&] {
+    if (at.threads > 32)
+      __syncthreads();
+    else
+      __syncwarp();
+  };
+  sync_row();  // what the row's threads stored
+  if (again == 0) return;
+  int buf = 0;
+  const int rows = static_cast<int>(P.rows);
+  for (int row = at.cta * at.groups + at.tid_y; row < rows; row += at.ctas * at.groups)
+    if (static_cast<const volatile float*>(P.scale)[row] == kRowAgain) {
+      sync_row();  // all have read it
+      norm_row_from_memory<E, MODE>(P, row, at.tid_x, at.threads, red, buf);
+    }
 }
 
 // Rows of up to NV vectors per thread.  A group of blockDim.x threads (a
@@ -395,6 +537,7 @@ __device__ __forceinline__ float row_scale(float sq, uint32_t top, float inv, in
 // not aligned.
 constexpr int kRowVecs = 4;
 constexpr int kRowScalars = 16;
+constexpr int kRowGroups = 8;     // rows of one warp that share a block
 constexpr int kRowThreads = 512;  // of a block that walks a row in two passes
 // Registers per thread, and the threads per SM they leave room for, 1024 or 512:
 // 64 KiB of loads in flight, or 32 and the next row's (the norms hold the
@@ -428,11 +571,17 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
   // Element by element there is no room for it, and it is read for each row.
   constexpr bool kHoldWeight = MODE != kRowQuant && VEC > 1;
   __shared__ uint2 red[2][32];
+  __shared__ int again;
+  if (threadIdx.x + threadIdx.y == 0) again = 0;
+  if (blockDim.y > 1) __syncthreads();  // its other writers: thread 0 of each group
   grid_dependency_wait();
   grid_dependency_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const long long first = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.y;
+  // (the norm's rows as ints: with two registers more the ragged one with a residual
+  // spills; those that are only quantised took 75 instead of 62 us so at [25600, 5120])
+  using Row = std::conditional_t<MODE == kRowQuant, long long, int>;
+  const Row first = static_cast<Row>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const Row stride = static_cast<Row>(gridDim.x) * blockDim.y, rows = static_cast<Row>(P.rows);
   // (where they start alike, they have the same vectors and loose elements)
   const RowSpan<VEC, RAGGED> span(first, P.d);
   const bool last_warp = RAGGED && warp == warps - 1;
@@ -451,7 +600,7 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
   int buf = 0;
   raw x[NV], t[MODE == kRowNormAdd ? NV : 1];
   raw1 xl = RV1::zero(), tl = RV1::zero();
-  auto load_row = [&](long long row) {
+  auto load_row = [&](Row row) {
     const size_t at = static_cast<size_t>(row) * P.d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -466,9 +615,9 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
         if constexpr (MODE == kRowNormAdd) tl = load_vec<E, 1>(P.residual, at + loose);
       }
   };
-  if (AHEAD && first < P.rows) load_row(first);  // before the weight's are waited for
+  if (AHEAD && first < rows) load_row(first);  // before the weight's are waited for
   if constexpr (kHoldWeight) load_weight();
-  for (long long row = first; row < P.rows; row += stride) {
+  for (Row row = first; row < rows; row += stride) {
     const size_t at = static_cast<size_t>(row) * P.d;
     if (!AHEAD) load_row(row);
     raw h[NV];
@@ -482,7 +631,7 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
     const raw1 hl = row_h<E, 1, MODE>(xl, tl);
     if constexpr (RAGGED && MODE == kRowNormAdd)
       if (loose >= 0) store_vec<E, 1>(P.h_out, at + loose, hl);
-    if (AHEAD && row + stride < P.rows) load_row(row + stride);
+    if (AHEAD && row + stride < rows) load_row(row + stride);
     if constexpr (MODE != kRowQuant && !kHoldWeight) load_weight();
     uint64_t sq2 = 0;
     float top1 = 0.f, sq;
@@ -493,8 +642,9 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
     if (last_warp) row_stats<E, 1, MODE>(hl, wl, sq2, top1);
     row_reduce(sq2, top1, warps, warp, lane, red[buf], sq, top);
     buf ^= 1;  // the slots are written again two rows on, past a barrier
-    const float inv = row_inv<MODE>(sq, top);
-    if (threadIdx.x == 0) P.scale[row] = row_scale<MODE>(sq, top, inv, P.d, P.eps);
+    const float inv = row_inv<MODE>(sq, top, P.eps);
+    if (threadIdx.x == 0)
+      P.scale[row] = row_scale<MODE>(sq, top, inv, P.d, P.eps, again);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
@@ -506,6 +656,8 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
       if (loose >= 0 && DORA_BOUNDS_OK(loose < P.d))
         row_codes<E, 1, MODE>(hl, wl, inv, P.q + at + loose);
   }
+  if constexpr (MODE != kRowQuant)
+    norm_rows_again<E, MODE>(P, again, red);
 }
 
 // Rows longer than the registers hold: two passes over the row, the second
@@ -522,11 +674,15 @@ __global__ void __launch_bounds__(kRowThreads, 2) row_quant_long_kernel(const Ro
   using raw1 = typename RV1::raw;
   constexpr int U = MODE == kRowNormAdd ? kRowLongVecs / 2 : kRowLongVecs;
   __shared__ uint2 red[2][32];
+  __shared__ int again;
+  if (threadIdx.x == 0) again = 0;
   grid_dependency_wait();
   grid_dependency_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int buf = 0;
-  for (long long row = blockIdx.x; row < P.rows; row += gridDim.x) {
+  using Row = std::conditional_t<MODE == kRowQuant, long long, int>;
+  const Row rows = static_cast<Row>(P.rows);
+  for (Row row = blockIdx.x; row < rows; row += gridDim.x) {
     const RowSpan<VEC, RAGGED> span(row, P.d);
     const size_t at = static_cast<size_t>(row) * P.d;
     const bool last_warp = RAGGED && warp == warps - 1;
@@ -574,8 +730,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) row_quant_long_kernel(const Ro
     if (last_warp) row_stats<E, 1, MODE>(hl, wl, sq2, top1);
     row_reduce(sq2, top1, warps, warp, lane, red[buf], sq, top);
     buf ^= 1;
-    const float inv = row_inv<MODE>(sq, top);
-    if (threadIdx.x == 0) P.scale[row] = row_scale<MODE>(sq, top, inv, P.d, P.eps);
+    const float inv = row_inv<MODE>(sq, top, P.eps);
+    if (threadIdx.x == 0)
+      P.scale[row] = row_scale<MODE>(sq, top, inv, P.d, P.eps, again);
     for (int c0 = threadIdx.x; c0 < span.vecs; c0 += U * blockDim.x) {
       raw h[U];
 #pragma unroll
@@ -596,6 +753,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) row_quant_long_kernel(const Ro
       if (loose >= 0 && DORA_BOUNDS_OK(loose < P.d))
         row_codes<E, 1, MODE>(hl, wl, inv, P.q + at + loose);
   }
+  if constexpr (MODE != kRowQuant)
+    norm_rows_again<E, MODE>(P, again, red);
 }
 
 // The values that codes stand for: x = q scale, one rounding.  A stream in the
