@@ -16,7 +16,8 @@
 //
 // Sums, maxima and products are fp32; h is rounded to the dtype because it is
 // stored and read again by the next layer, and the norm is of that stored
-// value.  A sum of squares beyond fp32's range counts as not finite.
+// value.  A row whose sum of squares, or whose scale, is beyond fp32's range
+// counts as not finite.
 #pragma once
 
 #include <type_traits>
@@ -462,7 +463,9 @@ __device__ __forceinline__ void norm_row_from_memory(const RowArgs& P, int row, 
   float inv = 0.f, scale = 0.f;
   if (__uint_as_float(top) >= kCodeMax * kMinNormal) {
     scale = __fmul_rn(norm_scale(sq, top, d, P.eps), lift == 1.f ? 1.f : 1.f / kRowLift);
-    if (scale >= kMinNormal)
+    if (__float_as_uint(scale) >= kInfBits || norm_rstd(sq, d, P.eps) == 0.f)
+      scale = __uint_as_float(0x7fc00000u);  // the scale, or mean + eps, is beyond fp32
+    else if (scale >= kMinNormal)
       inv = code_factor(__uint_as_float(top));
     else
       scale = 0.f;

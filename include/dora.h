@@ -361,8 +361,8 @@ dora_status_t dora_dequantize_rows(const int8_t *q, const float *scale, dora_dty
  *   v = h weight / sqrt(mean(h^2) + eps);  q, scale from v as above
  * The norm is of the stored h.  x, residual, h_out [T, d] and weight [d] in
  * `dt`; q [T, d]; scale [T] fp32; eps > 0 and finite.  Sums and products are
- * fp32: a row whose sum of squares, or whose h weight, passes fp32's range
- * counts as not finite.  h_out may equal x or residual (element for element);
+ * fp32: a row whose sum of squares (or its mean with eps), whose h weight or
+ * whose scale passes fp32's range counts as not finite.  h_out may equal x or residual (element for element);
  * no other overlap.  T == 0 launches nothing.  T, d <= 2^30.  One launch; x
  * (and the residual) are read once up to 16384 bf16 or 8192 fp32 elements a
  * row.  Alignment as above, and weight 16-byte aligned. */

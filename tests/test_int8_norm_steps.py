@@ -86,3 +86,34 @@ def test_neighbours_of_such_rows_keep_their_bits(d):
     assert torch.equal(q[keep], q0[keep]) and torch.equal(s[keep], s0[keep])
     _check(tiny[-5:], w, 1e-6, q[1::3][-5:], s[1::3][-5:], "tiny rows")
     _check(tiny[:5], w, 1e-6, q[1::3][:5], s[1::3][:5], "tiny rows")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [40000, 80000])
+def test_a_scale_beyond_fp32_is_not_finite(d, dt):
+    """Codes never stand for infinities: a row whose scale, or whose mean square
+    with eps, leaves fp32's range is held like one that is not finite.  The first
+    row's scale is 2^127 sqrt(d) / 127: 2.7e38 at 40000, 3.8e38 at 80000, where
+    fp32 ends at 3.4e38."""
+    x = torch.zeros(3, d)
+    x[0, 7] = 0.125          # v = 2^127 sqrt(d) at one place
+    x[1] = 0.125             # v = 2^127
+    x[2, ::2] = -0.125
+    x = x.to(DTYPES[dt]).cuda()
+    w = torch.full((d,), 2.0 ** 127, dtype=DTYPES[dt], device="cuda")
+    for residual in (None, torch.zeros_like(x)):
+        q, scale, _ = dora.dora_rmsnorm_quant(x, w, 1e-30, residual=residual)
+        v = oracle.rmsnorm(x.double().cpu().numpy(), w.double().cpu().numpy(), 1e-30)
+        _, s_ref, _ = oracle.quantize_rows(v)
+        first = 0 if d == 40000 else 1
+        if first:
+            assert torch.isnan(scale[0]) and not q[0].any()
+        else:
+            assert q[0, 7] == 127 and int(q[0].abs().sum()) == 127
+        # a thread's chain of terms, ten levels and six more roundings
+        tol = ((d / 512 + 8 + 12) / 2 + 6) * U
+        assert (np.abs(scale.double().cpu().numpy() - s_ref) <= tol * s_ref)[first:].all()
+        assert (q[1] == 127).all() and (q[2, ::2] == -127).all() and not q[2, 1::2].any()
+    h = torch.full((1, 1), 1.5e19, dtype=DTYPES[dt], device="cuda")
+    q, scale, _ = dora.dora_rmsnorm_quant(h, torch.ones_like(h[0]), 3e38)
+    assert torch.isnan(scale).all() and not q.any()
