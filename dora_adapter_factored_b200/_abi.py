@@ -40,7 +40,7 @@ EXPORTED = (
     "dora_compose_bwd_grouped", "dora_merge_weight_workspace_size", "dora_merge_weight",
     "dora_factored_norm_sq", "dora_norm_finalize", "dora_compose_fwd_delta",
     "dora_norm_plan_check", "dora_quantize_rows", "dora_dequantize_rows", "dora_rmsnorm_quant",
-    "dora_linear_i8_workspace_size", "dora_linear_i8",
+    "dora_linear_i8_workspace_size", "dora_linear_i8", "dora_linear_i8_plan",
 )
 
 
@@ -60,6 +60,12 @@ class NormProblem(ctypes.Structure):
         ("d_out", ctypes.c_int64), ("d_in", ctypes.c_int64), ("r", ctypes.c_int64),
         ("s", ctypes.c_float),
     ]
+
+
+class LinearPlan(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in (
+        "kernel", "padded", "tokens", "token_tiles", "channel_tiles", "splits", "kblocks",
+        "stages", "partials_over_ring", "group")]
 
 
 class ComposeProblem(ctypes.Structure):
@@ -172,6 +178,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.dora_linear_i8.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_i, c_i64, c_i64, c_i64,
                                        c_vp, c_vp, c_sz, c_vp]
         lib.dora_linear_i8.restype = c_i
+        lib.dora_linear_i8_plan.argtypes = [c_i64, c_i64, c_i64, c_i, c_i, c_i,
+                                            ctypes.POINTER(LinearPlan)]
+        lib.dora_linear_i8_plan.restype = c_i
         _lib = lib
         return lib
 
@@ -753,6 +762,19 @@ def dora_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float,
 
 def dora_linear_i8_workspace_size(T: int, d_out: int, d_in: int) -> int:
     return int(load_library().dora_linear_i8_workspace_size(T, d_out, d_in))
+
+
+def dora_linear_i8_plan(T: int, d_out: int, d_in: int, sms: int = 0, clusters4: int = 0,
+                        clusters8: int = 0) -> dict:
+    """How dora_linear_i8 runs a shape, by the fields of dora_linear_plan_t in
+    include/dora.h.  `sms` and the clusters of 4 and 8 CTAs that are resident at
+    once describe a device (148, 33 and 14 are near a B200's); 0 takes the
+    current one."""
+    plan = LinearPlan()
+    _check(load_library().dora_linear_i8_plan(int(T), int(d_out), int(d_in), int(sms),
+                                              int(clusters4), int(clusters8), ctypes.byref(plan)),
+           "dora_linear_i8_plan")
+    return {name: getattr(plan, name) for name, _ in LinearPlan._fields_}
 
 
 def dora_linear_i8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor,

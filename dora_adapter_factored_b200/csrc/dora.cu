@@ -2248,11 +2248,22 @@ size_t tmem_smem_floor(uint32_t cols) {
   return std::max<size_t>(cols * kSmemPerTmemCol - 1024, size_t(64) << 10);
 }
 
-// How the tensor-core path runs a shape: single CTAs or pairs, tokens per
-// tile, CTAs (pairs) that share a tile's k.
+// The ring of k-block stages in shared memory and the partials of a split k.
+struct I8Ring {
+  int stages;
+  uint32_t part_off;
+  bool part_over_ring;
+  size_t bytes;
+};
+
+// How a shape is run: dot products, or on the tensor cores (from padded copies
+// of the operands or as they are) by single CTAs or pairs, with the tokens per
+// tile and the CTAs (pairs) that share a tile's k.
 struct LinearPlan {
-  bool pair;
+  bool dot, pads, pair;
   int n, tiles_m, tiles_n, splits, kb;
+  int group;  // pairs: token tiles that go together
+  I8Ring ring;
 };
 
 // Two CTAs share an SM where there are more CTAs than SMs.
@@ -2358,13 +2369,6 @@ double estimate_dot_us(long long T, long long d_out, long long d_in) {
 // over the ring, at the price of a cluster barrier before they are written.
 // (Behind a ring of four 32 KiB stages a k-block took 0.42 us, not 0.26.)
 constexpr size_t kI8MinStages = 6;
-struct I8Ring {
-  int stages;
-  uint32_t part_off;
-  bool part_over_ring;
-  size_t bytes;
-};
-
 I8Ring plan_i8_ring(size_t room, size_t stage, const LinearPlan& p) {
   const size_t part = i8_partial_bytes(p.n, p.splits);
   // (a persistent pair's ring runs on into its next tile)
@@ -2380,6 +2384,42 @@ I8Ring plan_i8_ring(size_t room, size_t stage, const LinearPlan& p) {
   return r;
 }
 
+I8Ring tile_i8_ring(const LinearPlan& p, int sms) {
+  const size_t dyn =
+      tile_i8_shares_sm(p, sms) ? (size_t(113) << 10) - sizeof(TileI8Tail) : kTileI8MaxDynSmem;
+  return plan_i8_ring(dyn - 1024, kI8WBytes + static_cast<size_t>(p.n) * kI8K, p);
+}
+I8Ring pair_i8_ring(const LinearPlan& p) {
+  return plan_i8_ring(kPairI8MaxDynSmem - 1024, kI8WBytes + static_cast<size_t>(p.n / 2) * kI8K,
+                      p);
+}
+
+// Token tiles that go together: their codes stay in L2 while the weight
+// streams past.
+constexpr size_t kPairI8GroupBytes = size_t(32) << 20;
+int pair_i8_group(const LinearPlan& p, int ld) {
+  const size_t fit = std::max<size_t>(1, kPairI8GroupBytes / (static_cast<size_t>(p.n) * ld));
+  return static_cast<int>(ceil_div_ll(p.tiles_n, ceil_div_ll(p.tiles_n, fit)));  // evened out
+}
+
+// The whole plan of a call.  `vec`: rows of both operands are whole 16-byte
+// steps from a boundary.  Dot products: few tokens, where they are faster; rows
+// that are not of whole 16-byte steps, where few; and any number of rows that
+// are, but start off a boundary (TMA cannot read those, and the workspace, sized
+// from the shape, has no room for copies).
+LinearPlan choose_linear(int T, int d_out, int d_in, bool vec, const DeviceInfo& d) {
+  const bool pads = linear_pads(T, d_out, d_in);
+  double us = 0.0;
+  LinearPlan p{};
+  if (vec || pads) p = plan_linear(T, d_out, d_in, d, &us);
+  p.pads = pads;
+  p.dot = (vec && T <= kDotMaxT && estimate_dot_us(T, d_out, d_in) < us) || (!vec && !pads);
+  if (p.dot) return p;
+  p.ring = p.pair ? pair_i8_ring(p) : tile_i8_ring(p, d.sms);
+  if (p.pair) p.group = pair_i8_group(p, pads ? padded_k(d_in) : d_in);
+  return p;
+}
+
 template <typename O>
 dora_status_t launch_tile_i8(const LinearPlan& p, const LinearArgs& A, const int8_t* xq,
                              const int8_t* wq, int ld, int sms, cudaStream_t cs) {
@@ -2393,8 +2433,7 @@ dora_status_t launch_tile_i8(const LinearPlan& p, const LinearArgs& A, const int
   P.tmem_cols = 32;
   while (P.tmem_cols < static_cast<uint32_t>(p.n)) P.tmem_cols *= 2;
   P.idesc = idesc_i8_s32(kI8M, p.n);
-  const size_t dyn = tile_i8_shares_sm(p, sms) ? (size_t(113) << 10) - sizeof(TileI8Tail) : kTileI8MaxDynSmem;
-  const I8Ring r = plan_i8_ring(dyn - 1024, kI8WBytes + static_cast<size_t>(p.n) * kI8K, p);
+  const I8Ring& r = p.ring;
   P.stages = r.stages;
   P.ahead = ceil_div_ll(p.kb, p.splits) <= kTileI8ShortK
                 ? 0
@@ -2417,10 +2456,6 @@ dora_status_t launch_tile_i8(const LinearPlan& p, const LinearArgs& A, const int
   return launch_status();
 }
 
-// Token tiles that go together: their codes stay in L2 while the weight
-// streams past.
-constexpr size_t kPairI8GroupBytes = size_t(32) << 20;
-
 template <typename O>
 dora_status_t launch_pair_i8(const LinearPlan& p, const LinearArgs& A, const int8_t* xq,
                              const int8_t* wq, int ld, int sms, cudaStream_t cs) {
@@ -2433,11 +2468,9 @@ dora_status_t launch_pair_i8(const LinearPlan& p, const LinearArgs& A, const int
   P.kb = p.kb;
   P.tiles_m = p.tiles_m;
   P.tiles_n = p.tiles_n;
-  const size_t fit = std::max<size_t>(1, kPairI8GroupBytes / (static_cast<size_t>(p.n) * ld));
-  P.group = static_cast<int>(ceil_div_ll(p.tiles_n, ceil_div_ll(p.tiles_n, fit)));  // evened out
+  P.group = p.group;
   P.idesc = idesc_i8_s32(2 * kI8M, p.n);
-  const I8Ring r = plan_i8_ring(kPairI8MaxDynSmem - 1024,
-                                kI8WBytes + static_cast<size_t>(p.n / 2) * kI8K, p);
+  const I8Ring& r = p.ring;
   P.stages = r.stages;
   P.part_off = r.part_off;
   P.part_over_ring = r.part_over_ring;
@@ -2460,23 +2493,14 @@ dora_status_t launch_pair_i8(const LinearPlan& p, const LinearArgs& A, const int
 template <typename O>
 dora_status_t launch_linear(const LinearArgs& A, void* ws, const DeviceInfo& d, cudaStream_t cs) {
   const bool vec = A.d_in % 16 == 0 && aligned16(A.xq) && aligned16(A.wq);
-  const bool pads = linear_pads(A.T, A.d_out, A.d_in);
-  double us = 0.0;
-  LinearPlan p{};
-  if (vec || pads) p = plan_linear(A.T, A.d_out, A.d_in, d, &us);
-  // Dot products: few tokens, where they are faster; rows that are not of whole
-  // 16-byte steps, where few; and any number of rows that are, but start off a
-  // boundary (TMA cannot read those, and the workspace, sized from the shape,
-  // has no room for copies).
-  const bool few =
-      vec && A.T <= kDotMaxT && estimate_dot_us(A.T, A.d_out, A.d_in) < us;
-  if (few || (!vec && !pads)) {
+  const LinearPlan p = choose_linear(A.T, A.d_out, A.d_in, vec, d);
+  if (p.dot) {
     launch_dot_any<O>(A, vec, d.sms, cs);
     return launch_status();
   }
   const int8_t *xq = A.xq, *wq = A.wq;
   int ld = A.d_in;
-  if (pads) {
+  if (p.pads) {
     ld = padded_k(A.d_in);
     int8_t* xp = static_cast<int8_t*>(ws);
     int8_t* wp = xp + linear_pad_x(A.T, A.d_in);
@@ -2549,6 +2573,40 @@ size_t dora_linear_i8_workspace_size(int64_t T, int64_t d_out, int64_t d_in) {
       d_in > DORA_MAX_I8_K || !linear_pads(T, d_out, d_in))
     return 0;
   return linear_pad_x(T, d_in) + linear_pad_x(d_out, d_in);
+}
+
+dora_status_t dora_linear_i8_plan(int64_t T, int64_t d_out, int64_t d_in, int sms, int clusters4,
+                                  int clusters8, dora_linear_plan_t* plan) {
+  if (plan == nullptr || T < 1 || d_out < 1 || d_in < 1 || sms < 0) return DORA_ERR_INVALID_ARG;
+  if (sms > 0 && (clusters4 < 1 || clusters8 < 1)) return DORA_ERR_INVALID_ARG;
+  if (T > kMaxLinearTokens || d_out > kMaxQuantRows || d_in > DORA_MAX_I8_K)
+    return DORA_ERR_UNSUPPORTED;
+  DeviceInfo given;
+  given.sms = sms;
+  given.clusters4 = clusters4;
+  given.clusters8 = clusters8;
+  const DeviceInfo* d = &given;
+  if (sms == 0) {
+    d = device_info();
+    if (d == nullptr) return DORA_ERR_CUDA;
+    if (!d->supported) return DORA_ERR_UNSUPPORTED;
+    if (!ensure_tc_attrs()) return DORA_ERR_CUDA;
+  }
+  const LinearPlan p = choose_linear(static_cast<int>(T), static_cast<int>(d_out),
+                                     static_cast<int>(d_in), d_in % 16 == 0, *d);
+  *plan = {};
+  plan->kernel = p.dot ? 0 : p.pair ? 2 : 1;
+  if (p.dot) return DORA_OK;
+  plan->padded = p.pads;
+  plan->tokens = p.n;
+  plan->token_tiles = p.tiles_n;
+  plan->channel_tiles = p.tiles_m;
+  plan->splits = p.splits;
+  plan->kblocks = p.kb;
+  plan->stages = p.ring.stages;
+  plan->partials_over_ring = p.splits > 1 && p.ring.part_over_ring;
+  plan->group = p.group;
+  return DORA_OK;
 }
 
 dora_status_t dora_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq,

@@ -484,6 +484,24 @@ void dora_set_trace_buffer(void *buf);
  * dora_last_error(). */
 dora_status_t dora_norm_plan_check(const int64_t *d_out, const int64_t *d_in, const int64_t *r,
                                    int count, int grouped, int pairs);
+/* How dora_linear_i8 runs a shape (operands on 16-byte boundaries): host-only,
+ * the same code that chooses a launch.  `sms`, `clusters4` and `clusters8`
+ * describe a device (its SMs and the clusters of 4 and of 8 CTAs that are
+ * resident at once), so that no GPU is needed; sms == 0 takes the current one. */
+typedef struct {
+  int kernel;             /* 0 dot products (nothing else is set), 1 tiles of
+                             128 channels on single CTAs, 2 of 256 on CTA pairs */
+  int padded;             /* 1: from padded copies of the operands */
+  int tokens;             /* per tile */
+  int token_tiles, channel_tiles;
+  int splits;             /* CTAs or pairs that share a tile's k */
+  int kblocks;            /* of 128 codes */
+  int stages;             /* k-blocks on their way at once */
+  int partials_over_ring; /* a split k's partials reuse the stages' memory */
+  int group;              /* pairs: token tiles that go together */
+} dora_linear_plan_t;
+dora_status_t dora_linear_i8_plan(int64_t T, int64_t d_out, int64_t d_in, int sms,
+                                  int clusters4, int clusters8, dora_linear_plan_t *plan);
 /* Launches one thread that waits, with the same bounded wait the
  * tensor-core pipelines use, on a barrier that nothing ever signals, giving
  * up after `timeout_ns` (clamped to [1 us, 1 s]).  The give-up is recorded as
