@@ -700,8 +700,11 @@ __global__ void __launch_bounds__(kPairI8Threads)
     // to be consumed.
     for (long long j = issued > P.stages ? issued - P.stages : 0; j < issued; ++j) {
       const uint32_t par = static_cast<uint32_t>((j / P.stages) & 1);
-      mbar_wait(half == 0 ? &tail.full[j % P.stages] : &tail.empty[j % P.stages], par,
-                kDrainTimeoutNs, nullptr);
+      // (after a give-up a stage may never be filled by the peer or consumed: once
+      // this limit has passed, the copies issued before it have landed)
+      if (!mbar_wait(half == 0 ? &tail.full[j % P.stages] : &tail.empty[j % P.stages], par,
+                     kDrainTimeoutNs, nullptr))
+        break;
     }
   } else if (warp == kI8EpiWarps + 1) {
     // ------------------------------------------------------------- MMA issuer

@@ -110,12 +110,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
 }
 
 // As mbar_wait for waits in a pipeline's inner loop: the global timer is left
-// alone until some tries have failed.
+// alone until some tries have failed.  How long an untimed try is suspended is
+// the hardware's choice, so a limit that has no room for some is kept without.
+constexpr uint64_t kUntimedTriesNs = 100000000;  // 0.1 s; the default limit is 2 s
 __device__ __forceinline__ bool mbar_wait_fast(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
                                                const volatile int* abort) {
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, timeout_ns, abort);
+  if (timeout_ns >= kUntimedTriesNs)
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  const uint32_t hint = static_cast<uint32_t>(timeout_ns < 20000 ? timeout_ns : 20000);
+  while (!mbar_try_wait_sleep(bar, parity, hint)) {
+    if (abort != nullptr && *abort) return false;
+    if (global_timer_ns() - t0 > timeout_ns) return false;
+  }
+  return true;
 }
 
 // True in one lane of the (converged) warp, the same one every time.  Code
