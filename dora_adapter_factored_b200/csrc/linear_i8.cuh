@@ -542,7 +542,12 @@ __global__ void __launch_bounds__(kTileI8Threads)
     }
     const int* part = reinterpret_cast<const int*>(ring + P.part_off);
     i8_push_partials<S>(lane_base, P.n, warp, lane, slice, 1, 0, part);
+    // A slice that gave up leaves every sum of the tile incomplete.
+    if (*abort_flag != 0 && threadIdx.x < S)
+      st_cluster_u32(mapa_shared(smem_addr(&tail.abort_flag), threadIdx.x), 1u);
+    __syncwarp();
     cluster_sync();
+    if (*abort_flag != 0) out.ok = false;
     i8_finish_columns<S>(out, tail.sx, lane_base, P.n, warp, lane, slice, t0, part);
   }
   tc_fence_before_sync();
@@ -618,7 +623,6 @@ __global__ void __launch_bounds__(kPairI8Threads)
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank(), half = rank & 1u, lead = rank & ~1u;
   const int slice = static_cast<int>(rank >> 1);
-  const uint32_t peer_abort = mapa_shared(smem_addr(&tail.abort_flag), rank ^ 1u);
   const int kb0 = static_cast<int>(static_cast<long long>(slice) * P.kb / S);
   const int kb1 = static_cast<int>(static_cast<long long>(slice + 1) * P.kb / S);
   const uint32_t stage_bytes = kI8WBytes + static_cast<uint32_t>(P.n / 2) * kI8K;
@@ -627,8 +631,11 @@ __global__ void __launch_bounds__(kPairI8Threads)
   const int tiles = P.tiles_m * P.tiles_n;
   const int first = static_cast<int>(blockIdx.x) / (2 * S);
   const int step = static_cast<int>(gridDim.x) / (2 * S);
+  // Reaches every CTA of the cluster: a slice that gave up leaves every sum of the
+  // tile incomplete.
   auto give_up = [&] {
-    st_cluster_u32(peer_abort, 1u);
+    for (uint32_t r = 0; r < 2 * S; ++r)
+      if (r != rank) st_cluster_u32(mapa_shared(smem_addr(&tail.abort_flag), r), 1u);
     fence_cluster();  // there before this thread's part in the last barrier
     linear_give_up(abort_flag);
   };

@@ -386,7 +386,8 @@ dora_status_t dora_rmsnorm_quant(const void *x, const void *residual, const void
  * the call until it has run: two calls that overlap, or two captured graphs
  * that may, need one each).  With d_in a multiple of 16, xq and wq should be
  * 16-byte aligned: otherwise the call is computed with dot products, right
- * but far slower for more than a few tokens.  Up to two launches. */
+ * but far slower for more than a few tokens.  Up to two launches.  Where a wait
+ * ran out (DORA_ERR_TIMEOUT), each element of y is either right or not written. */
 #define DORA_MAX_I8_K 131071
 size_t dora_linear_i8_workspace_size(int64_t T, int64_t d_out, int64_t d_in);
 dora_status_t dora_linear_i8(const int8_t *xq, const float *x_scale, const int8_t *wq,

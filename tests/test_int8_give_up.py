@@ -1,7 +1,8 @@
 """What the int8 linear layer does when a wait runs out: with a limit of 1 ns no
 epilogue waits as long as its tile's products take, whatever the kernel or the
 split.  Every kernel then gives up by itself (every wait is bounded; nothing is
-left out and nothing faults), the status says so, and the next call is right."""
+left out and nothing faults), the status says so, nothing is written that is
+not right, and the next call is right."""
 import pytest
 import torch
 
@@ -74,3 +75,38 @@ def test_a_limit_that_is_long_enough_changes_nothing():
     finally:
         dora.dora_set_wait_timeout_ns(0)
     assert bool((y == 8192.0).all())
+
+
+SPLIT = [form for form in SHAPES if form[1] > 1]
+
+
+@pytest.mark.parametrize("form", SPLIT, ids=str)
+def test_no_sum_of_a_split_k_is_stored_incomplete(form):
+    """Limits about as long as the products: some of the CTAs that share a tile's
+    k give up and others do not.  What the tile stores is right or nothing."""
+    T, d_out, d_in = SHAPES[form]
+    g = torch.Generator("cuda").manual_seed(d_in)
+    codes = lambda r, c: torch.randint(-128, 128, (r, c), dtype=torch.int8, device="cuda",
+                                       generator=g)
+    xq, wq = codes(T, d_in), codes(d_out, d_in)
+    sx, sw = torch.rand(T, device="cuda", generator=g) + 0.5, \
+        torch.rand(d_out, device="cuda", generator=g) + 0.5
+    ref = dora.dora_linear_i8(xq, sx, wq, sw, dtype=torch.float32)
+    assert dora.dora_get_device_status() == _abi.DORA_OK
+    unwritten = -12345.5
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    y = torch.empty_like(ref)
+    try:
+        for step in range(48):
+            flush.zero_()  # the operands come from memory, not from L2
+            y.fill_(unwritten)
+            torch.cuda.synchronize()
+            dora.dora_set_wait_timeout_ns(int(500 * 1.1 ** step))  # 0.5 to 44 us
+            dora.dora_linear_i8(xq, sx, wq, sw, y=y)
+            status = dora.dora_get_device_status()
+            right = y == ref
+            assert bool((right | (y == unwritten)).all()), f"step {step}"
+            assert status in (_abi.DORA_OK, _abi.DORA_ERR_TIMEOUT)
+            assert status == _abi.DORA_ERR_TIMEOUT or bool(right.all())
+    finally:
+        dora.dora_set_wait_timeout_ns(0)
