@@ -14,7 +14,7 @@ from ._abi import (  # noqa: F401
     dora_compose_fwd_train, dora_compose_fwd_delta, dora_debug_unsignalled_wait, dora_factored_norm,
     dora_factored_norm_grouped, dora_factored_norm_grouped_workspace_size,
     dora_factored_norm_sq, dora_factored_norm_workspace_size, dora_norm_finalize, dora_norm_plan_check,
-    dora_get_device_status, dora_launch_count, dora_linear_i8, dora_linear_i8_plan,
+    dora_get_device_status, dora_kernels_prepared, dora_launch_count, dora_linear_i8, dora_linear_i8_plan,
     dora_linear_i8_workspace_size,
     dora_merge_weight, dora_merge_weight_workspace_size, dora_set_timing_events, dora_set_trace_buffer, dora_set_wait_timeout_ns, dora_version,
     dora_dequantize_rows, dora_quantize_rows, dora_rmsnorm_quant, load_library, status_string,

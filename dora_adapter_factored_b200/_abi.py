@@ -41,6 +41,7 @@ EXPORTED = (
     "dora_factored_norm_sq", "dora_norm_finalize", "dora_compose_fwd_delta",
     "dora_norm_plan_check", "dora_quantize_rows", "dora_dequantize_rows", "dora_rmsnorm_quant",
     "dora_linear_i8_workspace_size", "dora_linear_i8", "dora_linear_i8_plan",
+    "dora_kernels_prepared",
 )
 
 
@@ -271,6 +272,12 @@ def dora_norm_plan_check(shapes: Sequence[Sequence[int]], grouped: bool = False,
     arr = [(ctypes.c_int64 * n)(*[int(x[k]) for x in shapes]) for k in range(3)]
     _check(load_library().dora_norm_plan_check(arr[0], arr[1], arr[2], n, int(bool(grouped)),
                                                int(pairs)), "dora_norm_plan_check")
+
+
+def dora_kernels_prepared() -> int:
+    """Which tensor-core kernels are set up on the current device: 1 the norm's
+    and the merge's, 2 the 8-bit product's, added up."""
+    return int(load_library().dora_kernels_prepared())
 
 
 def dora_debug_unsignalled_wait(timeout_ns: int, stream=None) -> None:

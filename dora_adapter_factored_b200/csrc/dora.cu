@@ -65,6 +65,7 @@ struct DeviceInfo {
   int sms = 0;
   bool attrs_set = false;
   int norm_pairs = 0;  // CTA pairs of the norm GEMM resident at once
+  bool linear_set = false;  // the 8-bit product's kernels, apart from those
   int clusters4 = 0;   // clusters of 4 and of 8 CTAs, one CTA per SM, resident at once
   int clusters8 = 0;
 };
@@ -771,9 +772,7 @@ bool ensure_tc_attrs() {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem)) !=
           cudaSuccess ||
       (e = cudaFuncSetAttribute(merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kMaxDynSmem)) != cudaSuccess ||
-      (e = linear_smem_attrs<float>()) != cudaSuccess ||
-      (e = linear_smem_attrs<__nv_bfloat16>()) != cudaSuccess) {
+                                kMaxDynSmem)) != cudaSuccess) {
     note_error("cudaFuncSetAttribute", e);
     return false;
   }
@@ -793,9 +792,29 @@ bool ensure_tc_attrs() {
     clusters = std::max(1, sms / 2);
   }
   d.norm_pairs = std::min(clusters, std::max(1, sms / 2));
+  d.attrs_set = true;
+  return true;
+}
+
+// The same for the 8-bit product: at its own first call, so that a process that
+// only adapts weights neither loads its kernels nor depends on them.
+bool ensure_linear_attrs() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  DeviceInfo& d = g_dev[dev];
+  if (d.linear_set) return true;
+  cudaError_t e;
+  if ((e = linear_smem_attrs<float>()) != cudaSuccess ||
+      (e = linear_smem_attrs<__nv_bfloat16>()) != cudaSuccess) {
+    note_error("cudaFuncSetAttribute", e);
+    return false;
+  }
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 2;
   d.clusters4 = resident_clusters(4, sms);
   d.clusters8 = resident_clusters(8, sms);
-  d.attrs_set = true;
+  d.linear_set = true;
   return true;
 }
 
@@ -2590,7 +2609,7 @@ dora_status_t dora_linear_i8_plan(int64_t T, int64_t d_out, int64_t d_in, int sm
     d = device_info();
     if (d == nullptr) return DORA_ERR_CUDA;
     if (!d->supported) return DORA_ERR_UNSUPPORTED;
-    if (!ensure_tc_attrs()) return DORA_ERR_CUDA;
+    if (!ensure_linear_attrs()) return DORA_ERR_CUDA;
   }
   const LinearPlan p = choose_linear(static_cast<int>(T), static_cast<int>(d_out),
                                      static_cast<int>(d_in), d_in % 16 == 0, *d);
@@ -2643,7 +2662,7 @@ dora_status_t dora_linear_i8(const int8_t* xq, const float* x_scale, const int8_
   if (di == nullptr) return DORA_ERR_CUDA;
   if (!di->supported) return DORA_ERR_UNSUPPORTED;
   if (T == 0) return DORA_OK;
-  if (!ensure_tc_attrs()) return DORA_ERR_CUDA;
+  if (!ensure_linear_attrs()) return DORA_ERR_CUDA;
   const LinearArgs P{xq, x_scale, wq, w_scale, bias, y, static_cast<int>(T), static_cast<int>(d_out),
                static_cast<int>(d_in)};
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
@@ -2723,6 +2742,17 @@ dora_status_t dora_norm_plan_check(const int64_t* d_out, const int64_t* d_in, co
     return DORA_ERR_INTERNAL;
   }
   return DORA_OK;
+}
+
+int dora_kernels_prepared(void) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= dora::kMaxDevices) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  std::lock_guard<std::mutex> lk(dora::g_dev_mu);
+  const dora::DeviceInfo& d = dora::g_dev[dev];
+  return (d.attrs_set ? 1 : 0) | (d.linear_set ? 2 : 0);
 }
 
 void dora_set_timing_events(void* before, void* after) {

@@ -441,6 +441,10 @@ const char *dora_last_error(void);
 int dora_version(void);
 /* Number of kernels this library has launched in this process. */
 uint64_t dora_launch_count(void);
+/* Which tensor-core kernels calls of this process have set up on the current
+ * device: 1 the norm's and the merge's, 2 the 8-bit product's, added up.  Each
+ * is set up by the first call that needs it. */
+int dora_kernels_prepared(void);
 /* Upper bound, in nanoseconds, on any single internal wait of the
  * tensor-core kernels (default 2e9).  0 restores the default.  Host-side
  * setting, applied to launches made after the call; exists so that tests can
