@@ -357,17 +357,22 @@ struct ModulePlan {
 
 // One accumulator chunk up to N = 256, else two equal chunks; each chunk's
 // slab rows are split evenly between the two CTAs in 8-row swizzle groups.
+// The product writes whole 32-column chunks of the accumulator, which is how
+// the epilogue reads it (rows of the slab past r read 0): a column that it left
+// unwritten would hold what an earlier kernel or module put there, and a NaN
+// times the zero that stands for B is one.  n_pad, by which the schedule counts,
+// is the width rounded to 16.
 void plan_n_side(int r, ModulePlan& p) {
   if (r <= 256) {
     p.n_pad = round_up_int(r, 16);
-    p.n0 = p.n_pad;
+    p.n0 = round_up_int(r, 32);
     p.n1 = 0;
   } else {
     p.n_pad = round_up_int(r, 32);
     p.n0 = p.n1 = p.n_pad / 2;
   }
   p.h0 = p.n0 / 2;
-  p.b_region = static_cast<uint32_t>(p.n_pad / 2 * 128);
+  p.b_region = static_cast<uint32_t>((p.n0 + p.n1) / 2 * 128);
   int tc = 32;
   while (tc < p.n_pad) tc <<= 1;
   p.tmem_cols = tc;
