@@ -17,7 +17,8 @@ from ._abi import (  # noqa: F401
     dora_get_device_status, dora_kernels_prepared, dora_launch_count, dora_linear_i8, dora_linear_i8_plan,
     dora_linear_i8_workspace_size,
     dora_merge_weight, dora_merge_weight_workspace_size, dora_set_timing_events, dora_set_trace_buffer, dora_set_wait_timeout_ns, dora_version,
-    dora_dequantize_rows, dora_quantize_rows, dora_rmsnorm_quant, load_library, status_string,
+    dora_dequantize_rows, dora_quantize_rows, dora_rmsnorm_quant, dora_row_span_check,
+    load_library, status_string,
 )
 
 from .sharded import (  # noqa: F401,E402

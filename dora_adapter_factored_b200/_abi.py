@@ -41,7 +41,7 @@ EXPORTED = (
     "dora_factored_norm_sq", "dora_norm_finalize", "dora_compose_fwd_delta",
     "dora_norm_plan_check", "dora_quantize_rows", "dora_dequantize_rows", "dora_rmsnorm_quant",
     "dora_linear_i8_workspace_size", "dora_linear_i8", "dora_linear_i8_plan",
-    "dora_kernels_prepared",
+    "dora_kernels_prepared", "dora_row_span_check",
 )
 
 
@@ -179,6 +179,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.dora_linear_i8.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_i, c_i64, c_i64, c_i64,
                                        c_vp, c_vp, c_sz, c_vp]
         lib.dora_linear_i8.restype = c_i
+        lib.dora_row_span_check.argtypes = [c_i, c_i64, c_i64]
+        lib.dora_row_span_check.restype = c_i
         lib.dora_linear_i8_plan.argtypes = [c_i64, c_i64, c_i64, c_i, c_i, c_i,
                                             ctypes.POINTER(LinearPlan)]
         lib.dora_linear_i8_plan.restype = c_i
@@ -272,6 +274,13 @@ def dora_norm_plan_check(shapes: Sequence[Sequence[int]], grouped: bool = False,
     arr = [(ctypes.c_int64 * n)(*[int(x[k]) for x in shapes]) for k in range(3)]
     _check(load_library().dora_norm_plan_check(arr[0], arr[1], arr[2], n, int(bool(grouped)),
                                                int(pairs)), "dora_norm_plan_check")
+
+
+def dora_row_span_check(vec: int, row: int, cols: int) -> None:
+    """Host-only self-check of the row kernels' index arithmetic for one ragged row
+    (see include/dora.h); raises DoraError naming the first invariant that fails."""
+    _check(load_library().dora_row_span_check(int(vec), int(row), int(cols)),
+           "dora_row_span_check")
 
 
 def dora_kernels_prepared() -> int:

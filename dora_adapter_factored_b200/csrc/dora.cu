@@ -2114,6 +2114,57 @@ void launch_rows_dt(const RowArgs& P, dora_dtype_t dt, int sms, cudaStream_t cs)
     launch_rows_vec<float, 4, MODE>(P, sms, cs);
 }
 
+// The self-check behind dora_row_span_check: the vectors, loose elements and
+// weight loads that the row kernels take for one ragged row.  Returns "" or the
+// first invariant that fails.
+template <int VEC>
+std::string check_row_span(long long row, int cols) {
+  char msg[200];
+  const RowSpan<VEC, true> span(row, cols);
+  const size_t at = static_cast<size_t>(row) * cols;
+  std::vector<int> seen(cols, 0);
+  auto fail = [&](const char* what, long long i) {
+    snprintf(msg, sizeof(msg), "row %lld of %d columns, vectors of %d: %s (%lld)", row, cols, VEC,
+             what, i);
+    return std::string(msg);
+  };
+  if (span.vecs > std::max(1, cols / VEC)) return fail("more vectors than a launch has room for", span.vecs);
+  if (span.loose < 0 || span.loose > 32) return fail("more loose elements than lanes", span.loose);
+  for (int c = 0; c < span.vecs; ++c) {
+    const size_t first = span.column(c);
+    if ((at + first) % VEC != 0) return fail("a vector off its boundary", c);
+    if (first + VEC > static_cast<size_t>(cols)) return fail("a vector past its row", c);
+    for (int e = 0; e < VEC; ++e) ++seen[first + e];
+    // The weight: elements [VEC - lead, 2 VEC - lead) of vectors k - 1 and k.
+    const int k = span.weight_vec(c);
+    for (int e = 0; e < VEC; ++e) {
+      const int i = VEC - span.lead + e, v = i < VEC ? k - 1 : k, in = i < VEC ? i : i - VEC;
+      const long long j = static_cast<long long>(v) * VEC + in;
+      if (j != static_cast<long long>(first) + e) return fail("the weight of another column", j);
+      if (in >= span.weight_count(v)) return fail("a weight that is not loaded", j);
+    }
+    for (int v = k - 1; v <= k; ++v)
+      if (span.weight_count(v) < 0 || span.weight_count(v) > VEC ||
+          (span.weight_count(v) > 0 && (v < 0 || v * VEC + span.weight_count(v) > cols)))
+        return fail("a load past the weight", v);
+  }
+  for (int e = 0; e < span.loose; ++e) {
+    const int j = span.loose_column(e);
+    if (j < 0 || j >= cols) return fail("a loose element outside its row", j);
+    ++seen[j];
+  }
+  for (int j = 0; j < cols; ++j)
+    if (seen[j] != 1) return fail("a column not taken once", j);
+  // Rows that a block walks, whole vectors of rows apart, start alike.
+  for (int i = 1; i <= 3; ++i) {
+    const RowSpan<VEC, true> other(row + static_cast<long long>(i) * VEC, cols);
+    if (other.lead != span.lead || other.head != span.head || other.vecs != span.vecs ||
+        other.loose != span.loose)
+      return fail("walked rows that start apart", i);
+  }
+  return "";
+}
+
 // Element alignment of a pointer that may be NULL.
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -2758,6 +2809,18 @@ int dora_kernels_prepared(void) {
   std::lock_guard<std::mutex> lk(dora::g_dev_mu);
   const dora::DeviceInfo& d = dora::g_dev[dev];
   return (d.attrs_set ? 1 : 0) | (d.linear_set ? 2 : 0);
+}
+
+dora_status_t dora_row_span_check(int vec, int64_t row, int64_t cols) {
+  if ((vec != 4 && vec != 8) || row < 0 || cols < 1) return DORA_ERR_INVALID_ARG;
+  if (row > dora::kMaxQuantRows || cols > (1 << 20)) return DORA_ERR_UNSUPPORTED;
+  const std::string err = vec == 4 ? dora::check_row_span<4>(row, static_cast<int>(cols))
+                                   : dora::check_row_span<8>(row, static_cast<int>(cols));
+  if (!err.empty()) {
+    snprintf(dora::t_last_error, sizeof(dora::t_last_error), "%s", err.c_str());
+    return DORA_ERR_INTERNAL;
+  }
+  return DORA_OK;
 }
 
 void dora_set_timing_events(void* before, void* after) {

@@ -223,17 +223,25 @@ __device__ __forceinline__ typename RowVec<E, VEC>::raw shift_in(
 template <int VEC, bool RAGGED>
 struct RowSpan {
   int d, lead, head, vecs, loose;
-  __device__ __forceinline__ RowSpan(long long row, int cols) : d(cols) {
+  __host__ __device__ __forceinline__ RowSpan(long long row, int cols) : d(cols) {
     lead = RAGGED ? static_cast<int>(static_cast<size_t>(row) * cols % VEC) : 0;
-    head = RAGGED ? min((VEC - lead) % VEC, cols) : 0;
+    head = RAGGED ? ((VEC - lead) % VEC < cols ? (VEC - lead) % VEC : cols) : 0;
     vecs = (cols - head) / VEC;
     loose = RAGGED ? cols - vecs * VEC : 0;
   }
-  __device__ __forceinline__ size_t column(int c) const {
+  __host__ __device__ __forceinline__ size_t column(int c) const {
     return static_cast<size_t>(c) * VEC + head;
   }
-  __device__ __forceinline__ int loose_column(int e) const {
+  __host__ __device__ __forceinline__ int loose_column(int e) const {
     return e < head ? e : vecs * VEC + e;
+  }
+  // Vector c takes the last `lead` elements of the weight's vector before this
+  // one, and the first of this one: column(c) = weight_vec(c) VEC - lead.
+  __host__ __device__ __forceinline__ int weight_vec(int c) const { return lead ? c + 1 : c; }
+  // How many elements of the weight's vector v there are.
+  __host__ __device__ __forceinline__ int weight_count(int v) const {
+    if (v < 0 || v * VEC >= d) return 0;
+    return v * VEC + VEC > d ? d - v * VEC : VEC;
   }
   // The weight at the columns of vector c: where rows are ragged, put together
   // from two vectors of the weight (element by element, each load of a warp
@@ -246,11 +254,12 @@ struct RowSpan {
       return *reinterpret_cast<const typename RV::raw*>(p + c * VEC);
     } else {
       auto whole = [&](int v) -> typename RV::raw {
-        if (v < 0 || v * VEC >= d) return RV::zero();
-        if (v * VEC + VEC > d) return load_first<E, VEC>(p + v * VEC, d - v * VEC);
+        const int n = weight_count(v);
+        if (n == 0) return RV::zero();
+        if (n < VEC) return load_first<E, VEC>(p + v * VEC, n);
         return *reinterpret_cast<const typename RV::raw*>(p + v * VEC);
       };
-      const int k = lead ? c + 1 : c;  // column(c) = k VEC - lead
+      const int k = weight_vec(c);
       return shift_in<E, VEC>(whole(k - 1), whole(k), lead);
     }
   }

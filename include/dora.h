@@ -489,6 +489,14 @@ void dora_set_trace_buffer(void *buf);
  * dora_last_error(). */
 dora_status_t dora_norm_plan_check(const int64_t *d_out, const int64_t *d_in, const int64_t *r,
                                    int count, int grouped, int pairs);
+/* Host-only self-check of how the row kernels (dora_quantize_rows,
+ * dora_rmsnorm_quant) take row `row` of a matrix whose rows of `cols` elements are
+ * no whole number of vectors of `vec` (8 bf16 or 4 fp32): with the kernels' own
+ * index arithmetic, every column is taken once, in whole vectors on their
+ * boundaries that stay inside the row and in loose elements, with the weight of
+ * the same column, loaded from inside the weight.  Returns as
+ * dora_norm_plan_check.  cols <= 2^20. */
+dora_status_t dora_row_span_check(int vec, int64_t row, int64_t cols);
 /* How dora_linear_i8 runs a shape (operands on 16-byte boundaries): host-only,
  * the same code that chooses a launch.  `sms`, `clusters4` and `clusters8`
  * describe a device (its SMs and the clusters of 4 and of 8 CTAs that are
