@@ -2042,7 +2042,9 @@ namespace {
 // keeps the kernels' int indices in range.
 constexpr int64_t kMaxQuantRows = int64_t(1) << 30;
 constexpr int64_t kMaxQuantCols = int64_t(1) << 30;
-constexpr int64_t kMaxLinearTokens = int64_t(1) << 23;  // token tiles are a grid's second axis
+// Tokens of a product: its tiles (64 tokens by 128 channels or more each) are
+// counted in an int, with room for any y that a device holds.
+constexpr int64_t kMaxLinearTokens = int64_t(1) << 23;
 
 // The most blocks an SM holds of any launch of the row kernels (64 threads of
 // 64 registers): their L1/shared split has room for them.
@@ -2359,9 +2361,11 @@ constexpr int kTileI8ShortK = 8;
 // pays its set-up, the epilogue of its columns and, with a split k, the
 // exchange of partials.  The constants are a fit to the measured times of all
 // plans on 12 weights from 512 x 512 to 25600 x 5120 at 4 to 1500 tokens (2600
-// plans); the plan it picks is on average 1 % slower than the fastest,
+// plans); the plan it picks is on average 1 % slower than the fastest of those,
 // where a fixed rule (pairs above 64 tokens with the widest tile) was 20 %
-// slower.
+// slower.  On 8 other weights, 640 x 1280 to 20480 x 5120, at 1 to 2000 tokens (112
+// shapes, 1480 plans): 1.4 % on average, and 19 % at the worst, three tokens at
+// 2560 x 10240, where dot products are faster (7.0 against 8.3 us).
 double estimate_linear_us(const LinearPlan& p, long long T, long long d_out, long long d_in,
                           const DeviceInfo& d) {
   const double n = p.n, S = p.splits;
@@ -2402,15 +2406,16 @@ double estimate_linear_us(const LinearPlan& p, long long T, long long d_out, lon
 
 // The fastest plan by that estimate: a tile of up to 64, 128, 192 or 256
 // tokens, evened out over the token tiles, on one CTA or a pair, with its k
-// whole or split two, four or eight ways.  (One CTA from 17 tokens up to 1024,
-// and tiles of up to 128; beyond, pairs won at every shape.)
+// whole or split two, four or eight ways.  (Single CTAs up to 1024 tokens, in tiles
+// of up to 128; pairs from 17 tokens on.  Beyond those the other won at every
+// shape.)
 LinearPlan plan_linear(int T, int d_out, int d_in, const DeviceInfo& d, double* us) {
   LinearPlan best{};
   *us = 0.0;
   for (int pair = 0; pair < 2; ++pair)
     for (int cap = 64; cap <= kI8MaxN; cap += 64) {
       if (cap > 64 && T <= cap - 64) break;
-      if (pair ? T <= 16 : (cap > 128 || T > 1024)) continue;
+      if (pair ? T <= 16 : (cap > kTileI8MaxN || T > 1024)) continue;
       LinearPlan p;
       p.pair = pair != 0;
       p.tiles_n = static_cast<int>(ceil_div_ll(T, cap));

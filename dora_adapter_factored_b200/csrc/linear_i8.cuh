@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kDotWarps * 32) dot_i8_kernel(const LinearArgs
 // accumulator and from what the others push into its shared memory.
 constexpr int kI8M = 128;  // channels per CTA (TMEM lanes)
 constexpr int kI8K = 128;  // codes per k-block: one 128-byte swizzle row
-constexpr int kI8MaxN = 256;
+constexpr int kI8MaxN = 256;  // tokens per tile of a pair
 constexpr int kI8MaxStages = 12;
 constexpr uint32_t kI8WBytes = kI8M * kI8K;  // 16 KiB of weight per stage and CTA
 
@@ -401,9 +401,10 @@ __device__ __forceinline__ void i8_finish_columns(const ChannelOut<O>& out, cons
 }
 
 // ------------------------------------------------ single CTAs: small batches
-// One tile of 128 channels by up to 256 tokens per CTA.  Not persistent: with
-// up to 113 KiB and 256 TMEM columns per CTA two CTAs share an SM, so one's
+// One tile of 128 channels by up to 128 tokens per CTA.  Not persistent: with
+// up to 113 KiB and 128 TMEM columns per CTA two CTAs share an SM, so one's
 // epilogue runs beside the other's stream.
+constexpr int kTileI8MaxN = 128;  // tokens
 constexpr int kTileI8Threads = kI8EpiWarps * 32;
 
 struct alignas(64) TileI8Dev {
@@ -423,7 +424,7 @@ struct TileI8Tail {
   uint64_t full[kI8MaxStages];
   uint64_t empty[kI8MaxStages];
   uint64_t acc;
-  alignas(16) float sx[kI8MaxN];
+  alignas(16) float sx[kTileI8MaxN];
   uint32_t tmem_slot;
   int abort_flag;
 };

@@ -769,9 +769,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) row_quant_long_kernel(const Ro
     norm_rows_again<E, MODE>(P, again, red);
 }
 
-// The values that codes stand for: x = q scale, one rounding.  A stream in the
-// shape of the compose kernels: a thread keeps its columns and walks rows,
-// several rows' codes in flight.
+// The values that codes stand for: x = q scale in fp32, then rounded to the
+// dtype.  A stream in the shape of the compose kernels: a thread keeps its
+// columns and walks rows, several rows' codes in flight.
 constexpr int kDequantRowUnroll = 8;
 
 template <typename E, int VEC>

@@ -347,8 +347,8 @@ dora_status_t dora_merge_weight(const void *W0, const void *A, const void *B, co
 dora_status_t dora_quantize_rows(const void *x, dora_dtype_t dt, int64_t rows, int64_t cols,
                                  int8_t *q, float *scale, dora_stream_t stream);
 
-/* The values that codes stand for: x[i, j] = q[i, j] scale[i], rounded once to
- * `dt`; NaN in a row whose scale is NaN.  For a weight held as codes that a
+/* The values that codes stand for: x[i, j] = q[i, j] scale[i], the fp32 product,
+ * for DORA_BF16 rounded to bf16; NaN in a row whose scale is NaN.  For a weight held as codes that a
  * call of this library reads in bf16 or fp32 (W0 of the norm and the merge), or
  * for what reads activations unquantised.  x [rows, cols] must not overlap q
  * or scale.  rows == 0 launches nothing.  rows, cols <= 2^30.  One launch. */
