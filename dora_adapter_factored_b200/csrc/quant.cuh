@@ -219,7 +219,7 @@ __device__ __forceinline__ typename RowVec<E, VEC>::raw shift_in(
 // last warp.  No vector reaches into another row, and there are never more
 // than d / VEC, so that a row of 2^n - 1 columns takes no more threads than one
 // of 2^n.  (With first and last vectors that were masked and stored by element:
-// 122 against 77 us at [8192, 8191] bf16 with a residual, 93 against 42 without.)
+// 122 against 78 us at [8192, 8191] bf16 with a residual, 93 against 41 without.)
 template <int VEC, bool RAGGED>
 struct RowSpan {
   int d, lead, head, vecs, loose;
@@ -584,8 +584,10 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
   constexpr bool kHoldWeight = MODE != kRowQuant && VEC > 1;
   __shared__ uint2 red[2][32];
   __shared__ int again;
-  if (threadIdx.x + threadIdx.y == 0) again = 0;
-  if (blockDim.y > 1) __syncthreads();  // its other writers: thread 0 of each group
+  if constexpr (MODE != kRowQuant) {
+    if (threadIdx.x + threadIdx.y == 0) again = 0;
+    if (blockDim.y > 1) __syncthreads();  // its other writers: thread 0 of each group
+  }
   grid_dependency_wait();
   grid_dependency_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -675,7 +677,7 @@ __global__ void __maxnreg__(REGS) row_quant_kernel(const RowArgs P) {
 // Rows longer than the registers hold: two passes over the row, the second
 // from L2 (of h, as this thread stored it, where there is a residual), with a
 // few vectors on their way at a time (one by one [4096, 14336] fp32 took 80 us, 147
-// with a residual, against 65 and 131; with the weight's as well they spill, 129
+// with a residual, against 65 and 133; with the weight's as well they spill, 129
 // and 274).
 constexpr int kRowLongVecs = 4;  // half that of two streams
 template <typename E, int VEC, int MODE, bool RAGGED>
