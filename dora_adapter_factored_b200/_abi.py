@@ -4,13 +4,15 @@ Argument marshalling only: torch tensors are checked (device, dtype,
 contiguity), their data pointers, sizes and the current CUDA stream are
 passed to the library, and a non-OK status raises ``DoraError``.  Outputs and
 workspaces that the caller does not pass are allocated with torch (device
-memory plumbing); every step of the computation runs in the library's CUDA
+memory plumbing) on the stream that the call runs on; every step of the computation runs in the library's CUDA
 kernels.  There is no fallback: if libdora.so cannot be loaded, every call
 raises.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 from typing import Optional, Sequence
@@ -223,6 +225,31 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _on_stream(stream):
+    """Context in which what a call allocates belongs to the stream it runs on:
+    torch gives a workspace that the call drops only to later work of that
+    stream."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) \
+            else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _allocates(fn):
+    """A call whose outputs and workspace, where the caller passes none, are
+    allocated on its `stream`."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return fn(*args, **kwargs)
+        with _on_stream(stream):
+            return fn(*args, **kwargs)
+    return call
+
+
 def _check(status: int, where: str):
     if status != DORA_OK:
         raise DoraError(status, where)
@@ -302,6 +329,7 @@ def dora_factored_norm_workspace_size(d_out: int, d_in: int, r: int, dtype: torc
     return int(load_library().dora_factored_norm_workspace_size(d_out, d_in, r, _DT[dtype]))
 
 
+@_allocates
 def dora_factored_norm(W0: torch.Tensor, A: torch.Tensor, B: torch.Tensor, s: float,
                        m: Optional[torch.Tensor] = None, eps: float = 0.0,
                        n_out: Optional[torch.Tensor] = None, g_out: Optional[torch.Tensor] = None,
@@ -353,6 +381,7 @@ def dora_factored_norm_grouped_workspace_size(items: Sequence[dict]) -> int:
     return int(load_library().dora_factored_norm_grouped_workspace_size(arr, len(items), DORA_BF16))
 
 
+@_allocates
 def dora_factored_norm_grouped(items: Sequence[dict], eps: float = 0.0,
                                ws: Optional[torch.Tensor] = None, stream=None):
     """Grouped norm over modules given as dicts with keys W0, A, B, s, n_out and
@@ -366,6 +395,7 @@ def dora_factored_norm_grouped(items: Sequence[dict], eps: float = 0.0,
            "dora_factored_norm_grouped")
 
 
+@_allocates
 def dora_compose_fwd(base: torch.Tensor, lora: torch.Tensor, m: torch.Tensor, n: torch.Tensor,
                      s: float, eps: float = 0.0, y: Optional[torch.Tensor] = None, stream=None):
     """y = base + (g - 1) base + g s lora with g = m / max(n, eps)."""
@@ -382,6 +412,7 @@ def dora_compose_fwd(base: torch.Tensor, lora: torch.Tensor, m: torch.Tensor, n:
     return y
 
 
+@_allocates
 def dora_compose_fwd_delta(base: torch.Tensor, lora: torch.Tensor, m: torch.Tensor,
                            n: torch.Tensor, s: float, eps: float = 0.0,
                            dy_out: Optional[torch.Tensor] = None, stream=None):
@@ -404,6 +435,7 @@ def dora_compose_bwd_workspace_size(T: int, d_out: int, dtype: torch.dtype) -> i
     return int(load_library().dora_compose_bwd_workspace_size(T, d_out, _DT[dtype]))
 
 
+@_allocates
 def dora_compose_bwd(dy: torch.Tensor, base: torch.Tensor, lora: torch.Tensor, m: torch.Tensor,
                      n: torch.Tensor, s: float, eps: float = 0.0,
                      d_base: Optional[torch.Tensor] = None, d_lora: Optional[torch.Tensor] = None,
@@ -429,6 +461,7 @@ def dora_compose_bwd(dy: torch.Tensor, base: torch.Tensor, lora: torch.Tensor, m
     return d_base, d_lora, dm
 
 
+@_allocates
 def dora_compose_bwd_static(dy: torch.Tensor, base: torch.Tensor, lora: torch.Tensor,
                             m: torch.Tensor, n: torch.Tensor, s: float, eps: float = 0.0,
                             d_base: Optional[torch.Tensor] = None,
@@ -453,6 +486,7 @@ def dora_compose_bwd_static(dy: torch.Tensor, base: torch.Tensor, lora: torch.Te
     return d_base, d_lora, dm
 
 
+@_allocates
 def dora_compose_fwd_train(base: torch.Tensor, lora: torch.Tensor, m: torch.Tensor,
                            n: torch.Tensor, s: float, eps: float = 0.0,
                            y: Optional[torch.Tensor] = None, inner: Optional[torch.Tensor] = None,
@@ -471,6 +505,7 @@ def dora_compose_fwd_train(base: torch.Tensor, lora: torch.Tensor, m: torch.Tens
     return y, inner
 
 
+@_allocates
 def dora_compose_bwd_inner(dy: torch.Tensor, inner: torch.Tensor, m: torch.Tensor,
                            n: torch.Tensor, s: float, eps: float = 0.0,
                            d_base: Optional[torch.Tensor] = None,
@@ -496,6 +531,7 @@ def dora_compose_bwd_inner(dy: torch.Tensor, inner: torch.Tensor, m: torch.Tenso
     return d_base, d_lora, dm
 
 
+@_allocates
 def dora_compose_bwd_frozen(dy: torch.Tensor, m: torch.Tensor, n: torch.Tensor, s: float,
                             eps: float = 0.0, d_base: Optional[torch.Tensor] = None,
                             d_lora: Optional[torch.Tensor] = None, stream=None):
@@ -550,6 +586,7 @@ def dora_compose_bwd_grouped_workspace_size(items: Sequence[dict]) -> int:
     return int(load_library().dora_compose_bwd_grouped_workspace_size(arr, len(items), dt))
 
 
+@_allocates
 def dora_compose_bwd_grouped(items: Sequence[dict], eps: float = 0.0,
                              ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """Backward of several modules (dicts with dy, m, n, s, d_base, d_lora and
@@ -568,6 +605,7 @@ def dora_merge_weight_workspace_size(d_out: int, d_in: int, r: int) -> int:
     return int(load_library().dora_merge_weight_workspace_size(d_out, d_in, r))
 
 
+@_allocates
 def dora_merge_weight(W0: torch.Tensor, A: torch.Tensor, B: torch.Tensor, m: torch.Tensor,
                       n: torch.Tensor, s: float, eps: float = 0.0,
                       W_out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
@@ -588,6 +626,7 @@ def dora_merge_weight(W0: torch.Tensor, A: torch.Tensor, B: torch.Tensor, m: tor
     return W_out
 
 
+@_allocates
 def dora_factored_norm_sq(W0: torch.Tensor, A: torch.Tensor, B: torch.Tensor, s: float,
                           sq_out: Optional[torch.Tensor] = None,
                           ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -608,6 +647,7 @@ def dora_factored_norm_sq(W0: torch.Tensor, A: torch.Tensor, B: torch.Tensor, s:
     return sq_out
 
 
+@_allocates
 def dora_norm_finalize(sq: torch.Tensor, m: Optional[torch.Tensor] = None, eps: float = 0.0,
                        n_out: Optional[torch.Tensor] = None,
                        g_out: Optional[torch.Tensor] = None, stream=None):
@@ -675,14 +715,6 @@ def _current(stream, index: int) -> int:
     return _stream(stream)
 
 
-def _on_stream(stream, like: torch.Tensor):
-    """Context in which what a call allocates belongs to the stream it runs on."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) \
-            else torch.cuda.default_stream(like.device)
-    return torch.cuda.stream(stream)
-
-
 def _out_matrix(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dtype, index: int,
                 stream):
     """An output of `like`'s shape, the caller's or a new one: (tensor, pointer)."""
@@ -691,7 +723,7 @@ def _out_matrix(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dtype,
     if stream is None:
         t = torch.empty_like(like, dtype=dtype)
     else:
-        with _on_stream(stream, like):
+        with _on_stream(stream):
             t = torch.empty_like(like, dtype=dtype)
     return t, t.data_ptr()
 
@@ -704,7 +736,7 @@ def _out_vector(t: Optional[torch.Tensor], name: str, like: torch.Tensor, n: int
     if stream is None:
         t = like.new_empty(n, dtype=dtype)
     else:
-        with _on_stream(stream, like):
+        with _on_stream(stream):
             t = like.new_empty(n, dtype=dtype)
     return t, t.data_ptr()
 
@@ -821,7 +853,7 @@ def dora_linear_i8(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor,
         if stream is None:
             y = torch.empty(T, d_out, dtype=dtype, device=xq.device)
         else:
-            with _on_stream(stream, xq):
+            with _on_stream(stream):
                 y = torch.empty(T, d_out, dtype=dtype, device=xq.device)
         py = y.data_ptr()
     pws, nws = None, 0
