@@ -11,6 +11,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <string>
 #include <utility>
 #include <vector>
@@ -925,6 +926,39 @@ dora_status_t check_problem(const dora_norm_problem_t& p) {
   return DORA_OK;
 }
 
+// A copy that is captured reads its host source at every replay.  While `st` is
+// being captured, *src becomes a copy of `table` that the graph keeps: it is
+// freed with the last executable made from it.
+bool keep_for_capture(const std::vector<NormProblemDev>& table, cudaStream_t st,
+                      const NormProblemDev** src) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  cudaGraph_t graph = nullptr;
+  cudaError_t e = cudaStreamGetCaptureInfo_v2(st, &status, nullptr, &graph, nullptr, nullptr);
+  if (e == cudaSuccess && status == cudaStreamCaptureStatusNone) return true;
+  using Table = std::vector<NormProblemDev>;
+  if (e == cudaSuccess && status == cudaStreamCaptureStatusActive) {
+    Table* kept = new (std::nothrow) Table(table);
+    cudaUserObject_t owner = nullptr;
+    e = kept == nullptr ? cudaErrorMemoryAllocation
+                        : cudaUserObjectCreate(
+                              &owner, kept, [](void* p) { delete static_cast<Table*>(p); }, 1,
+                              cudaUserObjectNoDestructorSync);
+    if (e != cudaSuccess) {
+      delete kept;
+    } else {
+      *src = kept->data();
+      e = cudaGraphRetainUserObject(graph, owner, 1, cudaGraphUserObjectMove);
+      if (e != cudaSuccess) cudaUserObjectRelease(owner, 1);
+    }
+  } else if (e == cudaSuccess) {
+    e = cudaErrorStreamCaptureInvalidated;
+  }
+  if (e == cudaSuccess) return true;
+  (void)cudaGetLastError();
+  note_error("module table of a captured call", e);
+  return false;
+}
+
 dora_status_t run_tc_group(const dora_norm_problem_t* probs, int count, bool grouped, float eps,
                            void* ws, size_t ws_bytes, cudaStream_t st, bool emit_sq = false) {
   const DeviceInfo* di = device_info();
@@ -959,9 +993,15 @@ dora_status_t run_tc_group(const dora_norm_problem_t* probs, int count, bool gro
   const NormProblemDev* table = nullptr;
   if (grouped) {
     NormProblemDev* ntab = reinterpret_cast<NormProblemDev*>(base);
-    if (cudaMemcpyAsync(ntab, nds.data(), sizeof(NormProblemDev) * count,
-                        cudaMemcpyHostToDevice, st) != cudaSuccess)
+    const NormProblemDev* src = nds.data();
+    if (!keep_for_capture(nds, st, &src)) return DORA_ERR_CUDA;
+    const cudaError_t e = cudaMemcpyAsync(ntab, src, sizeof(NormProblemDev) * count,
+                                          cudaMemcpyHostToDevice, st);
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();
+      note_error("copy of the module table", e);
       return DORA_ERR_CUDA;
+    }
     table = ntab;
   }
   // One-warp blocks (each fits beside a fused-kernel CTA), as many as the

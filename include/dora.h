@@ -105,7 +105,8 @@ dora_status_t dora_factored_norm(const void *W0, const void *A, const void *B,
  * per stage.  `problems` is a HOST array of `count` descriptors, read during
  * the call only; the pointers inside are device pointers.  Per problem, m and
  * g_out may be NULL (then g is not written).  All problems share `dt` and
- * `eps`.  1 <= count <= DORA_MAX_GROUP.  bf16 only.
+ * `eps`.  1 <= count <= DORA_MAX_GROUP.  bf16 only.  A call that is captured
+ * into a graph leaves a host copy of its table with the graph.
  * ---------------------------------------------------------------------- */
 typedef struct {
   const void *W0;   /* [d_out, d_in] */
