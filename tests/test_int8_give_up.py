@@ -22,7 +22,7 @@ SHAPES = {
     ("tile", 8, 1): (3, 2316, 32768),
     ("pair", 1, 0): (1500, 4096, 4096),
     ("pair", 2, 0): (333, 2048, 8192),
-    ("pair", 2, 1): (199, 5677, 23072),
+    ("pair", 2, 1): (199, 5677, 23088),
     ("pair", 4, 0): (1063, 200, 14800),
     ("pair", 4, 1): (172, 2341, 87584),
 }

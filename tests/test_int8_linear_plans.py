@@ -37,7 +37,7 @@ SHAPES = [
     (333, 1024, 14336), (1040, 133, 6208), (1063, 200, 14800), (2825, 135, 11648),
     (1143, 130, 1761), (1063, 131, 6113),
     # ... and over it
-    (199, 5677, 23072), (172, 2341, 87584), (1063, 302, 14800),
+    (199, 5677, 23088), (172, 2341, 87584), (1063, 302, 14800),
 ]
 
 # (SMs, resident clusters of 4 CTAs, of 8): a B200 had 33 and 15
